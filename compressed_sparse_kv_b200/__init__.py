@@ -7,6 +7,7 @@ no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -19,7 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libdsv4kv.so")
 
 BF16, FP8_E4M3_ROW, FP4_E2M1_G16, FP8_E4M3_ROW_ROPE_BF16 = 0, 1, 2, 3
 DEV_BAD_INDEX, DEV_TIMEOUT, DEV_INCONSISTENT, DEV_BAD_POOL = 0x1, 0x2, 0x4, 0x8
-DEV_BAD_PAGE, DEV_BAD_LENGTH = 0x10, 0x20
+DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_NO_PAGES, DEV_BAD_TREE = 0x10, 0x20, 0x40, 0x80
 STATUS_NAMES = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED", 3: "ERR_WORKSPACE", 4: "ERR_CUDA"}
 
 
@@ -38,6 +39,11 @@ class PagedDesc(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("dim", ctypes.c_int32), ("page_rows", ctypes.c_int32),
                 ("table_stride", ctypes.c_int32), ("pool_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class PageTableDesc(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("page_rows", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("pool_pages", ctypes.c_int64)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -95,6 +101,28 @@ _SIGS = {
                                              _c.c_int32, _c.c_void_p, _c.c_int64, _c.c_int32, _c.c_int32,
                                              _c.c_float, _c.c_int32, _c.c_double, _c.c_int32, _c.c_void_p,
                                              _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "dsv4kv_paged_step_workspace_bytes": (_c.c_size_t, [_c.c_int32]),
+    "dsv4kv_block_table_update": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32,
+                                             _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_void_p,
+                                             _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                             _c.c_void_p]),
+    "dsv4kv_slot_map": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32,
+                                   _c.c_int32, _c.POINTER(PageTableDesc), _c.POINTER(PageTableDesc), _c.c_int64,
+                                   _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                   _c.c_size_t, _c.c_void_p]),
+    "dsv4kv_append_paged": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                       _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int32, _c.c_int32,
+                                       _c.c_int32, _c.c_int64, _c.c_int32, _c.c_double, _c.c_void_p,
+                                       _c.POINTER(PagedDesc), _c.POINTER(PagedDesc), _c.c_void_p, _c.c_size_t,
+                                       _c.c_void_p]),
+    "dsv4kv_tree_decode_paged_workspace_bytes": (_c.c_size_t, [_c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32,
+                                                               _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32,
+                                                               _c.c_int32]),
+    "dsv4kv_tree_decode_paged": (_c.c_int, [_c.c_void_p, _c.POINTER(PagedDesc), _c.POINTER(PagedDesc),
+                                            _c.POINTER(CacheDesc), _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32,
+                                            _c.c_int32, _c.c_int64, _c.c_int32, _c.c_void_p, _c.c_int64, _c.c_int32,
+                                            _c.c_int32, _c.c_int32, _c.c_float, _c.c_int32, _c.c_double, _c.c_int32,
+                                            _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "dsv4kv_dense_decode_workspace_bytes": (_c.c_size_t, [_c.c_int32, _c.c_int32, _c.c_int32, _c.c_int64,
                                                           _c.c_int32]),
     "dsv4kv_dense_decode": (_c.c_int, [_c.c_void_p, _c.POINTER(CacheDesc), _c.POINTER(CacheDesc), _c.c_int32,
@@ -168,6 +196,61 @@ class PagedCache:
     def desc(self) -> PagedDesc:
         return PagedDesc(self.fmt, self.dim, self.page_rows, int(self.table.shape[1]), self.pool_pages,
                          _ptr(self.table), _ptr(self.codes), _ptr(self.scales))
+
+
+@dataclass
+class PageTable:
+    """The page numbers of a cache without its rows (a PagedCache will do wherever one is taken)."""
+    table: torch.Tensor                      # int32 [B][table_stride]
+    page_rows: int
+    pool_pages: int
+
+
+@dataclass
+class SlotMap:
+    """Where the new tokens of a step go (slot_map): token i of the packed batch belongs to sequence seq[i] at position
+    pos[i]; win_slot / comp_slot are the pool rows that it writes (-1: none); cu[b] is sequence b's first token."""
+    cu: torch.Tensor                         # int32 [B + 1]
+    seq: torch.Tensor                        # int32 [capacity], -1 behind the last token
+    pos: torch.Tensor                        # int64 [capacity]
+    win_slot: torch.Tensor                   # int32 [capacity]
+    comp_slot: torch.Tensor                  # int32 [capacity]
+
+
+def _need(t, dtype, shape, where: str, name: str, device) -> None:
+    """Refuse a tensor that is not dense, of that type and shape (None: any size) and on the call's device."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or any(
+            w is not None and w != g for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor {list(shape)} on {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _on(device, stream):
+    """(context, stream handle) of a call: on its tensors' device and `stream`, or that device's current stream; what
+    the call allocates inside the context belongs to that stream."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream), stream.cuda_stream
+    here = device.index == torch.cuda.current_device()
+    return contextlib.nullcontext() if here else torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+
+
+_ROW_BYTES = {BF16: 1024, FP8_E4M3_ROW: 512, FP4_E2M1_G16: 256, FP8_E4M3_ROW_ROPE_BF16: 576}
+
+
+def _need_rows(c, rows, where: str, name: str, device) -> None:
+    """Refuse a 512-channel cache whose codes or scales are not dense, on the device and at least `rows` rows long."""
+    if c.dim != 512 or c.fmt not in _ROW_BYTES:
+        return                                # (the library's own refusal)
+    got = [("codes", c.codes, _ROW_BYTES[c.fmt])]
+    if c.fmt != BF16:
+        got.append(("scales", c.scales, 32 if c.fmt == FP4_E2M1_G16 else 4))
+    for what, t, per in got:
+        if t is None or t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < rows * per:
+            raise ValueError(f"{where}: {name}.{what} must be contiguous, on {device}, and hold {rows} rows")
 
 
 def new_workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -423,4 +506,167 @@ def dense_decode_paged(q: torch.Tensor, comp: PagedCache, win: PagedCache, t_seq
     _check(lib().dsv4kv_dense_decode_paged(_ptr(q), ctypes.byref(cd), ctypes.byref(wd), b, h, _ptr(t_seq), t_max,
                                            window, stride, sm_scale, rope_dim, rope_base, int(out_fp32), _ptr(out),
                                            _ptr(ws), ws.numel(), _stream(stream)), "dsv4kv_dense_decode_paged")
+    return out
+
+
+def paged_step_workspace_bytes(batch: int) -> int:
+    return int(lib().dsv4kv_paged_step_workspace_bytes(batch))
+
+
+def block_table_update(t_old: torch.Tensor, t_new: torch.Tensor, pages, free_pages: torch.Tensor,
+                       free_count: torch.Tensor, t_max: int, window: int = 128, stride: int = 4, lookahead: int = 0,
+                       free_count_out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """Take pages for the sequences that grow from t_old to t_new (int64 [B]) and give back those of the ones that
+    shrink: pages (PageTable or PagedCache) gets its table rows filled in place, free_pages int32 [cap] is a stack of
+    free_count (int64 [1]) page numbers.  stride 0: the table of a window cache.  Returns the new count
+    (free_count_out; pass free_count itself to update it in place)."""
+    dev, b = t_old.device, int(t_old.shape[0])
+    where = "block_table_update"
+    _need(t_old, torch.int64, (None,), where, "t_old", dev)
+    _need(t_new, torch.int64, (b,), where, "t_new", dev)
+    table = pages.table
+    _need(table, torch.int32, (b, None), where, "table", dev)
+    _need(free_pages, torch.int32, (None,), where, "free_pages", dev)
+    _need(free_count, torch.int64, (1,), where, "free_count", dev)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        if free_count_out is None:
+            free_count_out = torch.empty_like(free_count)
+        _need(free_count_out, torch.int64, (1,), where, "free_count_out", dev)
+        if ws is None:
+            ws = new_workspace(16, dev)
+        _need(ws, torch.uint8, (None,), where, "ws", dev)
+        _check(lib().dsv4kv_block_table_update(
+            t_old.data_ptr(), t_new.data_ptr(), b, t_max, window, stride, lookahead, pages.page_rows, table.data_ptr(),
+            int(table.shape[1]), pages.pool_pages, free_pages.data_ptr(), int(free_pages.shape[0]),
+            free_count.data_ptr(), free_count_out.data_ptr(), ws.data_ptr(), ws.numel(), s), "dsv4kv_block_table_update")
+    return free_count_out
+
+
+def new_slot_map(batch: int, capacity: int, device=None) -> SlotMap:
+    e = lambda n, dt: torch.empty(n, dtype=dt, device=device or "cuda")  # noqa: E731
+    return SlotMap(e(batch + 1, torch.int32), e(capacity, torch.int32), e(capacity, torch.int64),
+                   e(capacity, torch.int32), e(capacity, torch.int32))
+
+
+def _need_slots(m: SlotMap, b: int, where: str, dev) -> int:
+    cap = int(m.seq.shape[0])
+    _need(m.cu, torch.int32, (b + 1,), where, "cu", dev)
+    for name, dt in (("seq", torch.int32), ("pos", torch.int64), ("win_slot", torch.int32), ("comp_slot", torch.int32)):
+        _need(getattr(m, name), dt, (cap,), where, name, dev)
+    return cap
+
+
+def _table_desc(p, b: int, where: str, name: str, dev):
+    if p is None:
+        return None
+    _need(p.table, torch.int32, (b, None), where, name, dev)
+    return ctypes.byref(PageTableDesc(p.table.data_ptr(), p.page_rows, int(p.table.shape[1]), p.pool_pages))
+
+
+def slot_map(t_old: torch.Tensor, t_new: torch.Tensor, comp, win, capacity: int, t_max: int, window: int = 128,
+             stride: int = 4, lookahead: int = 0, out: Optional[SlotMap] = None, ws: Optional[torch.Tensor] = None,
+             stream=None) -> SlotMap:
+    """Sequence, position and cache slots of the new tokens t_old[b] .. t_new[b] - 1 of every sequence, packed in
+    order of b; comp and win are PageTables or PagedCaches (comp may be None, win too when window is 0)."""
+    dev, b = t_old.device, int(t_old.shape[0])
+    where = "slot_map"
+    _need(t_old, torch.int64, (None,), where, "t_old", dev)
+    _need(t_new, torch.int64, (b,), where, "t_new", dev)
+    cd, wd = _table_desc(comp, b, where, "comp.table", dev), _table_desc(win, b, where, "win.table", dev)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = new_slot_map(b, capacity, dev)
+        if _need_slots(out, b, where, dev) != capacity:
+            raise ValueError(f"{where}: out holds {int(out.seq.shape[0])} tokens, capacity is {capacity}")
+        if ws is None:
+            ws = new_workspace(16, dev)
+        _need(ws, torch.uint8, (None,), where, "ws", dev)
+        _check(lib().dsv4kv_slot_map(
+            t_old.data_ptr(), t_new.data_ptr(), b, t_max, window, stride, lookahead, cd, wd, capacity,
+            out.cu.data_ptr(), out.seq.data_ptr(), out.pos.data_ptr(), out.win_slot.data_ptr(),
+            out.comp_slot.data_ptr(), ws.data_ptr(), ws.numel(), s), "dsv4kv_slot_map")
+    return out
+
+
+def append_paged(s_new: torch.Tensor, w: torch.Tensor, slots: SlotMap, raw_ring: torch.Tensor,
+                 win: Optional[PagedCache], comp: PagedCache, stride: int, window: int = 128, lookahead: int = 0,
+                 max_new: Optional[int] = None, rope_dim: int = 64, rope_base: float = 10000.0,
+                 ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Append the states s_new bf16 [capacity][512] of a slot map's tokens: raw_ring bf16 [B][window + K][512], the
+    window rows and the entries that are due (w f32 [K][512]) into the paged caches, in their format.  max_new: no
+    sequence has more new tokens (a tight one saves a launch)."""
+    dev, b, taps = s_new.device, int(raw_ring.shape[0]), int(w.shape[0])
+    where = "append_paged"
+    cap = _need_slots(slots, b, where, dev)
+    _need(s_new, torch.bfloat16, (cap, 512), where, "s_new", dev)
+    _need(w, torch.float32, (None, 512), where, "w", dev)
+    _need(raw_ring, torch.bfloat16, (None, window + taps, 512), where, "raw_ring", dev)
+    for name, c in (("comp", comp), ("win", win)):
+        if c is not None:
+            _need(c.table, torch.int32, (b, None), where, name + ".table", dev)
+            _need_rows(c, c.pool_pages * c.page_rows, where, name, dev)
+    ctx, s = _on(dev, stream)
+    with ctx:
+        if ws is None:
+            ws = new_workspace(16, dev)
+        _need(ws, torch.uint8, (None,), where, "ws", dev)
+        cd = comp.desc()
+        wd = ctypes.byref(win.desc()) if win is not None else None
+        _check(lib().dsv4kv_append_paged(
+            s_new.data_ptr(), w.data_ptr(), b, cap, slots.cu.data_ptr(), slots.seq.data_ptr(), slots.pos.data_ptr(),
+            slots.win_slot.data_ptr(), slots.comp_slot.data_ptr(), taps, stride, window, lookahead,
+            cap if max_new is None else max_new, rope_dim, rope_base, raw_ring.data_ptr(), wd, ctypes.byref(cd),
+            ws.data_ptr(), ws.numel(), s), "dsv4kv_append_paged")
+
+
+def tree_decode_paged_workspace_bytes(batch: int, heads: int, max_nodes: int, nodes: int, t_max: int, window: int = 128,
+                                      stride: int = 128, k: Optional[int] = None) -> int:
+    """k: places per node of the sparse form's idx, None for the dense form."""
+    return int(lib().dsv4kv_tree_decode_paged_workspace_bytes(batch, heads, 512, max_nodes, nodes, t_max, window,
+                                                              stride, k or 0))
+
+
+def tree_decode_paged(q: torch.Tensor, comp: PagedCache, win: PagedCache, draft: Cache, cu: torch.Tensor,
+                      parent: torch.Tensor, t_seq: torch.Tensor, t_max: int, max_nodes: int, window: int = 128,
+                      stride: int = 128, idx: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None,
+                      rope_dim: int = 64, rope_base: float = 10000.0, out_fp32: bool = False,
+                      out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over paged caches: q bf16 [nodes][H][512] and the rows of draft (codes
+    [1][nodes][...]) packed by sequence (cu int32 [B + 1]); parent int32 [nodes] numbers within the sequence, -1 for a
+    child of the last cached token.  idx int32 [nodes][k]: each node's selected entries (c4a); None: all (c128a)."""
+    n, h, d = q.shape
+    dev, b = q.device, int(t_seq.shape[0])
+    where = "tree_decode_paged"
+    _need(q, torch.bfloat16, (n, h, 512), where, "q", dev)
+    _need(cu, torch.int32, (b + 1,), where, "cu", dev)
+    _need(parent, torch.int32, (n,), where, "parent", dev)
+    _need(t_seq, torch.int64, (b,), where, "t_seq", dev)
+    for name, c in (("comp", comp), ("win", win)):
+        _need(c.table, torch.int32, (b, None), where, name + ".table", dev)
+        _need_rows(c, c.pool_pages * c.page_rows, where, name, dev)
+    _need_rows(draft, n, where, "draft", dev)
+    k = 0
+    if idx is not None:
+        _need(idx, torch.int32, (n, None), where, "idx", dev)
+        k = int(idx.shape[1])
+    if sm_scale is None:
+        sm_scale = d ** -0.5
+    ctx, s = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((n, h, d), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=dev)
+        _need(out, torch.float32 if out_fp32 else torch.bfloat16, (n, h, 512), where, "out", dev)
+        if ws is None:
+            ws = new_workspace(tree_decode_paged_workspace_bytes(b, h, max_nodes, n, t_max, window, stride, k), dev)
+        _need(ws, torch.uint8, (None,), where, "ws", dev)
+        cd, wd = comp.desc(), win.desc()
+        dd = CacheDesc(draft.fmt, draft.dim, n, _ptr(draft.codes), _ptr(draft.scales))
+        _check(lib().dsv4kv_tree_decode_paged(
+            q.data_ptr(), ctypes.byref(cd), ctypes.byref(wd), ctypes.byref(dd), cu.data_ptr(), parent.data_ptr(),
+            _ptr(idx), b, h, n, max_nodes, t_seq.data_ptr(), t_max, window, stride, k, sm_scale, rope_dim, rope_base,
+            int(out_fp32), out.data_ptr(), ws.data_ptr(), ws.numel(), s), "dsv4kv_tree_decode_paged")
     return out

@@ -464,6 +464,216 @@ DSV4KV_API dsv4kv_status dsv4kv_dense_decode_paged(const void* q, const dsv4kv_p
                       sm_scale, rope_dim, rope_base, out_fp32, out, ws, ws_bytes, stream);
 }
 
+// ------------------------------------------------------------------ paged serving step
+static constexpr int64_t kMaxLen = int64_t(1) << 30;
+static constexpr int32_t kMaxWindow = 65536;
+
+DSV4KV_API size_t dsv4kv_paged_step_workspace_bytes(int32_t batch) {
+  return batch < 0 ? 0 : 16;  // the status word and a counter
+}
+
+static dsv4kv_status check_step(const char* what, int32_t batch, const int64_t* t_old, const int64_t* t_new,
+                                int64_t t_max, int32_t window, int32_t lookahead, const void* ws, size_t ws_bytes) {
+  if (batch < 0 || t_max < 0 || window < 0) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  if (lookahead < 0 || lookahead > window)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: lookahead must be in [0, window]", what);
+  if (batch > 4096) return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: batch must be <= 4096", what);
+  if (t_max >= kMaxLen || window > kMaxWindow)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: t_max must be < 2^30 and window <= 65536", what);
+  if (batch > 0 && (!t_old || !t_new)) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: lengths are null", what);
+  if (!ws || ws_bytes < 16 || !aligned16(ws))
+    return set_error(DSV4KV_ERR_WORKSPACE, "%s: workspace null, misaligned or too small", what);
+  return DSV4KV_OK;
+}
+
+// Rows of a cache of a sequence of t tokens (stride 0: a window cache).
+static int64_t step_rows(int64_t t, int32_t window, int32_t stride, int32_t lookahead) {
+  return stride == 0 ? std::min<int64_t>(t, window) : dsv4kv_compress_entries(t + lookahead, window, stride);
+}
+
+static dsv4kv_status check_table(const char* what, const int32_t* table, int32_t page_rows, int32_t table_stride,
+                                 int64_t pool_pages, int64_t max_rows) {
+  if (page_rows <= 0 || page_rows % 64 != 0)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: page_rows must be a positive multiple of 64", what);
+  if (pool_pages < 1 || pool_pages > ((int64_t(1) << 31) - 1) / page_rows)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the pool must hold between 1 page and 2^31 rows", what);
+  const int64_t need = (max_rows + page_rows - 1) / page_rows;
+  if (table_stride < need)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: table_stride %d < %lld pages a sequence may need", what, table_stride,
+                     (long long)need);
+  if (max_rows > 0 && !table) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: block table is null", what);
+  return DSV4KV_OK;
+}
+
+DSV4KV_API dsv4kv_status dsv4kv_block_table_update(const int64_t* t_old, const int64_t* t_new, int32_t batch,
+                                                   int64_t t_max, int32_t window, int32_t stride, int32_t lookahead,
+                                                   int32_t page_rows, int32_t* table, int32_t table_stride,
+                                                   int64_t pool_pages, int32_t* free_pages, int64_t free_cap,
+                                                   const int64_t* free_count, int64_t* free_count_out, void* ws,
+                                                   size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* what = "block_table_update";
+  dsv4kv_status st = check_step(what, batch, t_old, t_new, t_max, window, lookahead, ws, ws_bytes);
+  if (st != DSV4KV_OK) return st;
+  if (stride < 0) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: stride < 0", what);
+  const int64_t rows = step_rows(t_max, window, stride, lookahead);
+  st = check_table(what, table, page_rows, table_stride, pool_pages, rows);
+  if (st != DSV4KV_OK) return st;
+  if (int64_t(batch) * ((rows + page_rows - 1) / page_rows) >= (int64_t(1) << 31))
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: batch x pages must be < 2^31", what);
+  if (free_cap < 0 || (free_cap > 0 && !free_pages) || !free_count || !free_count_out)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: free list null or of negative size", what);
+  return block_table_update_launch(t_old, t_new, batch, t_max, window, stride, lookahead, page_rows, table, table_stride,
+                                   pool_pages, free_pages, free_cap, free_count, free_count_out, ws,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+DSV4KV_API dsv4kv_status dsv4kv_slot_map(const int64_t* t_old, const int64_t* t_new, int32_t batch, int64_t t_max,
+                                         int32_t window, int32_t stride, int32_t lookahead,
+                                         const dsv4kv_page_table* comp, const dsv4kv_page_table* win, int64_t capacity,
+                                         int32_t* cu, int32_t* seq, int64_t* pos, int32_t* win_slot,
+                                         int32_t* comp_slot, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* what = "slot_map";
+  dsv4kv_status st = check_step(what, batch, t_old, t_new, t_max, window, lookahead, ws, ws_bytes);
+  if (st != DSV4KV_OK) return st;
+  if (stride < 1) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: stride must be >= 1", what);
+  if (capacity < 0) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: capacity < 0", what);
+  if (capacity >= (int64_t(1) << 31) - 4096) return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: capacity too large", what);
+  if (!cu || (capacity > 0 && (!seq || !pos || !win_slot || !comp_slot || !aligned16(seq) || !aligned16(pos) ||
+                               !aligned16(win_slot) || !aligned16(comp_slot))))
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: output null or misaligned", what);
+  if (window > 0 && !win) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: window table is null", what);
+  PageDesc cp{nullptr, 64, 0, 0}, wp{nullptr, 64, 0, 0};
+  if (comp) {
+    st = check_table(what, comp->table, comp->page_rows, comp->table_stride, comp->pool_pages,
+                     step_rows(t_max, window, stride, lookahead));
+    if (st != DSV4KV_OK) return st;
+    cp = PageDesc{comp->table, comp->page_rows, comp->table_stride, comp->pool_pages};
+  }
+  if (window > 0) {
+    st = check_table(what, win->table, win->page_rows, win->table_stride, win->pool_pages,
+                     std::min<int64_t>(t_max, window));
+    if (st != DSV4KV_OK) return st;
+    wp = PageDesc{win->table, win->page_rows, win->table_stride, win->pool_pages};
+  }
+  return slot_map_launch(t_old, t_new, batch, t_max, window, stride, lookahead, cp, wp, int(capacity), cu, seq, pos,
+                         win_slot, comp_slot, ws, static_cast<cudaStream_t>(stream));
+}
+
+DSV4KV_API dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t batch, int64_t capacity,
+                                             const int32_t* cu, const int32_t* seq, const int64_t* pos,
+                                             const int32_t* win_slot, const int32_t* comp_slot, int32_t k_taps,
+                                             int32_t stride, int32_t window, int32_t lookahead, int64_t max_new,
+                                             int32_t rope_dim, double rope_base, void* raw_ring,
+                                             const dsv4kv_paged_cache* win, const dsv4kv_paged_cache* comp, void* ws,
+                                             size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* what = "append_paged";
+  if (batch < 0 || capacity < 0 || k_taps < 1 || stride < 1 || window < 0 || max_new < 0)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  if (lookahead < 0 || lookahead > window)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: lookahead must be in [0, window]", what);
+  if (window > kMaxWindow || k_taps > kMaxWindow || stride > (1 << 24) || capacity >= (int64_t(1) << 31) - 4096)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: sizes too large", what);
+  if (rope_dim < 0 || rope_dim > 512 || (rope_dim & 1))
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: rope_dim must be even and <= 512", what);
+  if (!(rope_base > 0.0)) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: rope_base must be > 0", what);
+  if (!ws || ws_bytes < 16 || !aligned16(ws))
+    return set_error(DSV4KV_ERR_WORKSPACE, "%s: workspace null, misaligned or too small", what);
+  if (batch == 0 || capacity == 0) return DSV4KV_OK;
+  if (!s_new || !w || !raw_ring || !aligned16(s_new) || !aligned16(w) || !aligned16(raw_ring))
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: null or misaligned pointer", what);
+  if (!cu || !seq || !pos || !win_slot || !comp_slot)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: slot map is null", what);
+  const dsv4kv_paged_cache* both[2] = {comp, win};
+  dsv4kv_cache pool[2] = {};
+  for (int i = 0; i < (window > 0 ? 2 : 1); ++i) {
+    const dsv4kv_paged_cache* c = both[i];
+    if (!c) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: paged cache descriptor is null", what);
+    if (c->fmt < DSV4KV_BF16 || c->fmt > DSV4KV_FP8_E4M3_ROW_ROPE_BF16)
+      return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: format %d", what, c->fmt);
+    dsv4kv_status st = check_table(what, c->table, c->page_rows, c->table_stride, c->pool_pages, 0);
+    if (st != DSV4KV_OK) return st;
+    pool[i] = dsv4kv_cache{c->fmt, c->dim, c->pool_pages * int64_t(c->page_rows), c->codes, c->scales};
+    st = check_cache(&pool[i], what, 1, 512);
+    if (st != DSV4KV_OK) return st;
+  }
+  if (window > 0 && win->fmt != comp->fmt)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the window cache must have the compressed cache's format", what);
+  if (comp->fmt == DSV4KV_FP8_E4M3_ROW_ROPE_BF16 && rope_dim != 64)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the fp8 + bf16 rotary format requires rope_dim == 64", what);
+  return append_paged_launch(s_new, w, batch, int(capacity), cu, seq, pos, win_slot, comp_slot, k_taps, stride, window,
+                             lookahead, max_new, rope_dim, rope_base, raw_ring, pool[1], pool[0], ws,
+                             static_cast<cudaStream_t>(stream));
+}
+
+static bool tree_sizes_ok(int32_t batch, int32_t heads, int32_t max_nodes, int64_t nodes, int64_t t_max, int32_t window,
+                          int32_t stride, int32_t k) {
+  return batch >= 1 && batch <= 1024 && heads >= 1 && heads <= 128 && max_nodes >= 1 && max_nodes <= 256 && nodes >= 0 &&
+         nodes < ((int64_t(1) << 31) - 1024) / heads && t_max >= 0 && t_max < kMaxLen && window >= 0 &&
+         window <= kMaxWindow && stride >= 1 && k >= 0 && k <= 2048;
+}
+
+DSV4KV_API size_t dsv4kv_tree_decode_paged_workspace_bytes(int32_t batch, int32_t heads, int32_t dim,
+                                                           int32_t max_nodes, int64_t nodes, int64_t t_max,
+                                                           int32_t window, int32_t stride, int32_t k) {
+  if (dim != 512 || !tree_sizes_ok(batch, heads, max_nodes, nodes, t_max, window, stride, k)) return 0;
+  return tree_ws_bytes(batch, heads, max_nodes, nodes, t_max, window, stride, k);
+}
+
+DSV4KV_API dsv4kv_status dsv4kv_tree_decode_paged(const void* q, const dsv4kv_paged_cache* comp,
+                                                  const dsv4kv_paged_cache* win, const dsv4kv_cache* draft,
+                                                  const int32_t* cu, const int32_t* parent, const int32_t* idx,
+                                                  int32_t batch, int32_t heads, int64_t nodes, int32_t max_nodes,
+                                                  const int64_t* t_seq, int64_t t_max, int32_t window, int32_t stride,
+                                                  int32_t k, float sm_scale, int32_t rope_dim, double rope_base,
+                                                  int32_t out_fp32, void* out, void* ws, size_t ws_bytes,
+                                                  void* stream) {
+  g_err[0] = 0;
+  const char* what = "tree_decode_paged";
+  dsv4kv_status st = check_ragged(what, batch, t_seq, t_max, window, stride);
+  if (st != DSV4KV_OK) return st;
+  if (nodes < 0 || max_nodes < 1) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  if (idx && (k < 1 || k > 2048)) return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: k must be in [1, 2048]", what);
+  if (!tree_sizes_ok(batch, heads, max_nodes, nodes, t_max, window, stride, idx ? k : 0))
+    return set_error(DSV4KV_ERR_UNSUPPORTED,
+                     "%s: batch must be <= 1024, heads <= 128, max_nodes <= 256, t_max < 2^30, window <= 65536", what);
+  if (rope_dim < 0 || rope_dim > 512 || (rope_dim & 1))
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: bad rope_dim", what);
+  if (!(rope_base > 0.0)) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: rope_base must be > 0", what);
+  if (!cu) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: cu is null", what);
+  // the deepest node stands max_nodes - 1 positions past the last cached token
+  const int64_t n_max = dsv4kv_compress_entries(t_max + max_nodes - 1, window, stride);
+  const int32_t w_max = int32_t(std::min<int64_t>(t_max, window));
+  dsv4kv_cache cpool{}, wpool{};
+  PageDesc cpg{}, wpg{};
+  st = check_paged(comp, what, dsv4kv_compress_entries(t_max, window, stride), 512, false, &cpool, &cpg);
+  if (st != DSV4KV_OK) return st;
+  st = check_paged(win, what, w_max, 512, false, &wpool, &wpg);
+  if (st != DSV4KV_OK) return st;
+  if (n_max > 0) {  // (table entries past table_stride are bad pages to the kernel)
+    if (!cpg.table) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: block table is null", what);
+    st = check_cache(&cpool, what, 1, 512);
+    if (st != DSV4KV_OK) return st;
+  }
+  st = check_cache(draft, what, nodes, 512);
+  if (st != DSV4KV_OK) return st;
+  if (win->fmt != comp->fmt || draft->fmt != comp->fmt)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the three caches must have one format", what);
+  if (comp->fmt == DSV4KV_FP8_E4M3_ROW_ROPE_BF16 && rope_dim != 64)
+    return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the fp8 + bf16 rotary format requires rope_dim == 64", what);
+  if (!ws || !aligned16(ws) ||
+      ws_bytes < tree_ws_bytes(batch, heads, max_nodes, nodes, t_max, window, stride, idx ? k : 0))
+    return set_error(DSV4KV_ERR_WORKSPACE, "%s: workspace null, misaligned or too small", what);
+  if (nodes == 0) return DSV4KV_OK;
+  if (!q || !aligned16(q) || !out || !aligned16(out) || !parent)
+    return set_error(DSV4KV_ERR_INVALID_ARG, "%s: q/out/parent null or misaligned", what);
+  TreeArgs a{q, cpool, wpool, *draft, cpg, wpg, cu, parent, idx, batch, heads, nodes, max_nodes, t_seq, t_max, window,
+             stride, idx ? k : 0, sm_scale, rope_dim, rope_base, out_fp32, out};
+  return tree_decode_launch(a, ws, static_cast<cudaStream_t>(stream));
+}
+
 DSV4KV_API dsv4kv_status dsv4kv_dense_decode(const void* q, const dsv4kv_cache* comp, const dsv4kv_cache* win,
                                              int32_t batch, int32_t heads, int64_t n, int32_t window, int64_t t,
                                              float sm_scale, int32_t rope_dim, double rope_base, int32_t out_fp32,

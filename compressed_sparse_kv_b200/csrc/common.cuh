@@ -25,6 +25,21 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return uint32_t(f2bf(lo)) | (uint32_t(f2bf(hi)) << 16);
 }
 
+// Two fp32 -> bf16x2, round to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// cos / sin of pos * theta_m, theta_pi = theta_m / pi: the angle in units of
+// pi is reduced exactly modulo 2 in fp64, and the remainder (|x| <= 1, rounded
+// to fp32: 6e-8 absolute) goes to the fp32 functions.
+__device__ __forceinline__ void rope_rotation(double theta_pi, double pos, float* cs, float* sn) {
+  const double ang = pos * theta_pi;
+  sincospif(float(ang - 2.0 * rint(0.5 * ang)), sn, cs);
+}
+
 // Order-preserving map of a float to uint32 (larger float -> larger code);
 // -0 is mapped like +0 by the callers (they add 0.0f first).
 __device__ __forceinline__ uint32_t ord_f32(float f) {
@@ -210,6 +225,13 @@ __device__ __forceinline__ void bulk_load_plain(void* dst, const void* src, uint
                    smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int32_t c0,
                                             int32_t c1, int32_t c2) {

@@ -111,6 +111,47 @@ dsv4kv_status index_topk_launch(const uint16_t* qidx, const dsv4kv_cache& keys, 
                                 int32_t* idx_out, int32_t* count_out, void* ws, size_t ws_bytes,
                                 cudaStream_t stream);
 
+// rope_base^(-2m / rope_dim) / pi of every rotary pair, as a kernel argument.
+struct RopeTable {
+  double theta_pi[256];
+};
+void rope_table_fill(RopeTable* r, int rope_dim, double rope_base);
+
+dsv4kv_status block_table_update_launch(const int64_t* t_old, const int64_t* t_new, int batch, int64_t t_max, int window,
+                                        int stride, int lookahead, int page_rows, int32_t* table, int table_stride,
+                                        int64_t pool_pages, int32_t* free_pages, int64_t free_cap,
+                                        const int64_t* free_count, int64_t* free_count_out, void* ws,
+                                        cudaStream_t stream);
+dsv4kv_status slot_map_launch(const int64_t* t_old, const int64_t* t_new, int batch, int64_t t_max, int window,
+                              int stride, int lookahead, const PageDesc& comp, const PageDesc& win, int capacity,
+                              int32_t* cu, int32_t* seq, int64_t* pos, int32_t* win_slot, int32_t* comp_slot, void* ws,
+                              cudaStream_t stream);
+dsv4kv_status append_paged_launch(const void* s_new, const float* w, int batch, int tokens, const int32_t* cu,
+                                  const int32_t* seq, const int64_t* pos, const int32_t* win_slot,
+                                  const int32_t* comp_slot, int k_taps, int stride, int window, int lookahead,
+                                  int64_t max_new, int rope_dim, double rope_base, void* raw_ring,
+                                  const dsv4kv_cache& win, const dsv4kv_cache& comp, void* ws, cudaStream_t stream);
+
+struct TreeArgs {
+  const void* q;
+  dsv4kv_cache comp, win, draft;  // comp, win: the pools (rows = pool rows)
+  PageDesc comp_pg, win_pg;
+  const int32_t *cu, *parent, *idx;  // idx null: dense
+  int batch, heads;
+  int64_t nodes;
+  int max_nodes;
+  const int64_t* t_seq;
+  int64_t t_max;
+  int window, stride, k;
+  float sm_scale;
+  int rope_dim;
+  double rope_base;
+  int out_fp32;
+  void* out;
+};
+size_t tree_ws_bytes(int batch, int heads, int max_nodes, int64_t nodes, int64_t t_max, int window, int stride, int k);
+dsv4kv_status tree_decode_launch(const TreeArgs& a, void* ws, cudaStream_t stream);
+
 struct DecodeArgs {
   const void* q;
   dsv4kv_cache comp;   // paged: codes / scales are the pools, rows = pool rows

@@ -1,0 +1,636 @@
+// The cache side of a paged serving step: block tables, slot maps, and the
+// append of a ragged batch's new tokens ([P1] hybrid KV cache manager
+// paragraph: blocks of a shared pool; "compressor-state blocks").
+//
+// block_table_kernel.  With pages(t) = ceil(rows(t) / page_rows), sequence b
+// gives back G_b = max(0, pages(t_old) - pages(t_new)) pages or takes
+// A_b = max(0, pages(t_new) - pages(t_old)).  Given-back pages are pushed on the
+// free stack in (b, entry) order, then A = sum A_b are popped in (b, entry)
+// order: taken page a is element count + G - 1 - a of the grown stack.  An
+// element past the old count is read where it comes from, in a shrinking
+// sequence's table row, so pushes and pops need no order between them and
+// one launch does both: every CTA forms the two prefix sums over the batch
+// (one pass of warp scans in shared memory) and takes a share of the pages.
+// The count is read by every CTA and written by the last one to finish, so
+// that it may be updated in place.
+//
+// slot_map_kernel.  Every CTA forms the prefix sums of the new tokens, then a
+// thread finds the sequence of its first token by binary search and walks on;
+// 4 tokens a thread, 16-byte stores.
+//
+// append_paged_kernel.  A CTA of 8 warps takes `per` consecutive tokens.  It
+// lists the tokens whose row stays in a ring and those that emit an entry; a
+// warp copies / rotates one row (16 channels a lane); entries of up to 32
+// taps are one warp's work, longer ones (c128a) are summed by all 8 warps,
+// tap j by warp j % 8, four entries at a time so that a weight row (2 KB) is
+// read once for four state rows, the warps' sums added in warp order.  The
+// work is bound by the state rows' HBM reads for whole prompts and by
+// latency for a decode step.  Entries read rows of the raw ring that tokens of the
+// same call replace when a sequence has more than lookahead + 1 new ones
+// (entry taps reach back to p + 1 + lookahead - (window + k_taps), the row
+// replaced by token p' is p' - (window + k_taps)); the ring is then written by
+// a second launch.
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "quant_row.cuh"
+
+namespace dsv4kv {
+
+namespace {
+
+constexpr int kTabThreads = 512;
+constexpr int kSlotThreads = 256;
+constexpr int kSlotPer = 4;  // tokens a thread
+
+// Exclusive prefix sums of f(b), b in [0, batch), into pre[0 .. batch] by all NT
+// threads; f packs two counts (low and high half), whose sums stay below 2^32.
+template <int NT, class F, class S>
+__device__ __forceinline__ uint64_t block_prefix(int batch, F f, S store) {
+  __shared__ uint64_t wsum[NT / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t carry = 0;
+  for (int b0 = 0; b0 < batch; b0 += NT) {
+    const int b = b0 + int(threadIdx.x);
+    const uint64_t v = b < batch ? f(b) : 0;
+    uint64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    uint64_t before = carry, all = carry;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+      if (i < warp) before += wsum[i];
+      all += wsum[i];
+    }
+    if (b < batch) store(b, before + x - v);
+    carry = all;
+    __syncthreads();
+  }
+  return carry;
+}
+
+// Largest b in [0, n) with pre[b] <= x (pre ascending, pre[0] = 0).
+__device__ __forceinline__ int find_seq(const int32_t* pre, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int64_t clamp_len(int64_t t, int64_t t_max, uint32_t* status) {
+  if (t >= 0 && t <= t_max) return t;
+  set_status(status, DSV4KV_DEV_BAD_LENGTH);
+  return t < 0 ? 0 : t_max;
+}
+
+struct TableParams {
+  const int64_t *t_old, *t_new;
+  int batch;
+  int64_t t_max;
+  int window, stride, lookahead, page_rows;
+  int32_t* table;
+  int table_stride;
+  int64_t pool_pages;
+  int32_t* free_pages;
+  int64_t free_cap;
+  const int64_t* free_count;
+  int64_t* free_count_out;
+  uint32_t* status;  // workspace: status word, then the count of finished CTAs
+};
+
+__device__ __forceinline__ int pages_of(const TableParams& p, int64_t t) {
+  const int x = int(t);  // t_max + lookahead < 2^31
+  const int rows = p.stride == 0 ? min(x, p.window) : max(0, x + p.lookahead - p.window) / p.stride;
+  return int((unsigned(rows) + unsigned(p.page_rows) - 1) / unsigned(p.page_rows));
+}
+
+__global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableParams p) {
+  extern __shared__ int32_t sm[];
+  int32_t *back = sm, *take = sm + p.batch + 1;  // prefix sums of the pages given back / taken
+  pdl_trigger();
+  pdl_wait();
+  int64_t count = *p.free_count;
+  if (count < 0 || count > p.free_cap) {
+    set_status(p.status, DSV4KV_DEV_BAD_LENGTH);
+    count = count < 0 ? 0 : p.free_cap;
+  }
+  const uint64_t sums = block_prefix<kTabThreads>(
+      p.batch,
+      [&](int b) -> uint64_t {
+        const int o = pages_of(p, clamp_len(p.t_old[b], p.t_max, p.status));
+        const int n = pages_of(p, clamp_len(p.t_new[b], p.t_max, p.status));
+        return o > n ? uint64_t(o - n) : uint64_t(n - o) << 32;
+      },
+      [&](int b, uint64_t v) {
+        back[b] = int32_t(v & 0xffffffffu);
+        take[b] = int32_t(v >> 32);
+      });
+  const int G = int(sums & 0xffffffffu), A = int(sums >> 32);
+  __syncthreads();
+  const int step = gridDim.x * kTabThreads, first = blockIdx.x * kTabThreads + int(threadIdx.x);
+  // the table entry that given-back page r comes from
+  auto given = [&](int r) -> int32_t {
+    const int b = find_seq(back, p.batch, r);
+    const int n = pages_of(p, clamp_len(p.t_new[b], p.t_max, nullptr));
+    return p.table[size_t(b) * p.table_stride + n + (r - back[b])];
+  };
+  for (int r = first; r < G; r += step) {
+    const int32_t pg = given(r);
+    if (pg < 0 || pg >= p.pool_pages) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+    if (count + r < p.free_cap) p.free_pages[count + r] = pg;
+    else set_status(p.status, DSV4KV_DEV_NO_PAGES);
+  }
+  const int64_t top = min(count + G, p.free_cap);  // the grown stack
+  for (int a = first; a < A; a += step) {
+    const int b = find_seq(take, p.batch, a);
+    const int o = pages_of(p, clamp_len(p.t_old[b], p.t_max, nullptr));
+    const int64_t at = top - 1 - a;
+    int32_t pg = -1;
+    if (at < 0) {
+      set_status(p.status, DSV4KV_DEV_NO_PAGES);
+    } else {
+      pg = at >= count ? given(int(at - count)) : p.free_pages[at];
+      if (pg < 0 || pg >= p.pool_pages) {
+        set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+        pg = -1;
+      }
+    }
+    p.table[size_t(b) * p.table_stride + o + (a - take[b])] = pg;
+  }
+  // the last CTA to get here (every CTA has read the count) writes it
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    uint32_t* done = p.status + 1;
+    if (atomicAdd(done, 1u) == gridDim.x - 1) {
+      *done = 0;
+      *p.free_count_out = max(int64_t(0), top - A);
+    }
+  }
+}
+
+struct SlotParams {
+  const int64_t *t_old, *t_new;
+  int batch;
+  int64_t t_max;
+  int window, stride, lookahead;
+  PageDesc comp, win;
+  int capacity;
+  int32_t *cu, *seq;
+  int64_t* pos;
+  int32_t *win_slot, *comp_slot;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ int32_t slot_of(const PageDesc& d, int b, int row, uint32_t* status) {
+  const int page = row / d.page_rows;
+  const int32_t pg = __ldg(d.table + size_t(b) * d.table_stride + page);
+  if (pg < 0 || pg >= d.pool_pages) {
+    set_status(status, DSV4KV_DEV_BAD_PAGE);
+    return -1;
+  }
+  return pg * d.page_rows + (row - page * d.page_rows);  // pool rows < 2^31
+}
+
+__global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams p) {
+  extern __shared__ int32_t pre[];  // first token of every sequence, clamped to the capacity
+  pdl_trigger();
+  pdl_wait();
+  const uint64_t sum = block_prefix<kSlotThreads>(
+      p.batch,
+      [&](int b) -> uint64_t {
+        const int64_t o = clamp_len(p.t_old[b], p.t_max, p.status), n = clamp_len(p.t_new[b], p.t_max, p.status);
+        return uint64_t(max(int64_t(0), n - o));
+      },
+      [&](int b, uint64_t v) {
+        pre[b] = int32_t(min(v, uint64_t(p.capacity)));
+        if (blockIdx.x == 0) p.cu[b] = pre[b];
+      });
+  const int total = int(min(sum, uint64_t(p.capacity)));
+  if (threadIdx.x == 0) {
+    pre[p.batch] = total;
+    if (blockIdx.x == 0) {
+      p.cu[p.batch] = total;
+      if (sum > uint64_t(p.capacity)) set_status(p.status, DSV4KV_DEV_BAD_LENGTH);
+    }
+  }
+  __syncthreads();
+  const int64_t stepw = int64_t(gridDim.x) * kSlotThreads * kSlotPer;
+  for (int64_t i0 = (int64_t(blockIdx.x) * kSlotThreads + threadIdx.x) * kSlotPer; i0 < p.capacity; i0 += stepw) {
+    int32_t sq[kSlotPer], ws[kSlotPer], cs[kSlotPer];
+    int64_t ps[kSlotPer];
+    int b = i0 < total ? find_seq(pre, p.batch, int(i0)) : 0;
+    int o = 0, n = 0, of = -1;
+#pragma unroll
+    for (int e = 0; e < kSlotPer; ++e) {
+      const int i = int(i0) + e;
+      sq[e] = ws[e] = cs[e] = -1;
+      ps[e] = -1;
+      if (i >= total) continue;
+      while (pre[b + 1] <= i) ++b;  // (ends: i < pre[batch])
+      if (of != b) {
+        o = int(clamp_len(p.t_old[b], p.t_max, nullptr));
+        n = int(clamp_len(p.t_new[b], p.t_max, nullptr));
+        of = b;
+      }
+      const int pp = o + (i - pre[b]);
+      sq[e] = b;
+      ps[e] = pp;
+      if (p.win.table && pp >= n - p.window) ws[e] = slot_of(p.win, b, pp % p.window, p.status);
+      const int r = pp + 1 + p.lookahead - p.window;  // the entry ends when it is a multiple of the stride
+      if (p.comp.table && r > 0 && r % p.stride == 0) cs[e] = slot_of(p.comp, b, r / p.stride - 1, p.status);
+    }
+    if (i0 + kSlotPer <= p.capacity) {
+      *reinterpret_cast<int4*>(p.seq + i0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
+      *reinterpret_cast<longlong2*>(p.pos + i0) = make_longlong2(ps[0], ps[1]);
+      *reinterpret_cast<longlong2*>(p.pos + i0 + 2) = make_longlong2(ps[2], ps[3]);
+      *reinterpret_cast<int4*>(p.win_slot + i0) = make_int4(ws[0], ws[1], ws[2], ws[3]);
+      *reinterpret_cast<int4*>(p.comp_slot + i0) = make_int4(cs[0], cs[1], cs[2], cs[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kSlotPer; ++e) {
+        if (i0 + e >= p.capacity) break;
+        p.seq[i0 + e] = sq[e];
+        p.pos[i0 + e] = ps[e];
+        p.win_slot[i0 + e] = ws[e];
+        p.comp_slot[i0 + e] = cs[e];
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ append
+constexpr int kAppWarps = 8;
+constexpr int kAppThreads = 32 * kAppWarps;
+constexpr int kD = 512, kPer = kD / 32;
+constexpr int kMaxTokens = 512;  // tokens a CTA
+constexpr int kGroup = 4;        // long entries summed together
+constexpr int kLongTaps = 32;    // entries of more taps are summed by the whole CTA
+
+enum : int { kPartEntries = 1, kPartWindow = 2, kPartRing = 4 };
+
+struct AppendParams {
+  const uint16_t* s_new;
+  const float* w;
+  int batch;
+  int tokens, per;  // packed tokens (capacity), tokens a CTA
+  const int32_t *cu, *seq;
+  const int64_t* pos;
+  const int32_t *win_slot, *comp_slot;
+  int k_taps, stride, window, lookahead, max_new, rope_dim, parts;
+  uint16_t* ring;
+  uint8_t *win_codes, *comp_codes;
+  void *win_scales, *comp_scales;
+  int64_t win_rows, comp_rows;  // pool rows
+  uint32_t* status;
+  RopeTable rope;
+};
+
+struct Tok {
+  int i, b, pos, first;  // token, sequence, position, the sequence's first new token
+};
+
+// x = channels [16 lane, 16 lane + 16) of a row, its rotary pairs rotated at pos.
+// theta: pair `lane`'s theta / pi (where there are at most 32 pairs).
+__device__ __forceinline__ void rotate_row(float (&x)[kPer], const AppendParams& p, double theta, int pos, int lane) {
+  const int r0 = kD - p.rope_dim, pairs = p.rope_dim / 2, c0 = kPer * lane;
+  if (pairs <= 32) {
+    // lane m computes pair m; the lanes that own rotary channels fetch theirs
+    float cs_m = 1.f, sn_m = 0.f;
+    if (lane < pairs) rope_rotation(theta, double(pos), &cs_m, &sn_m);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      const int m = (c0 + e - r0) >> 1;
+      const float cs = __shfl_sync(kFull, cs_m, m & 31), sn = __shfl_sync(kFull, sn_m, m & 31);
+      if (m >= 0) {
+        const float a = x[e], b = x[e + 1];
+        x[e] = a * cs - b * sn;
+        x[e + 1] = a * sn + b * cs;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      const int m = (c0 + e - r0) >> 1;
+      if (m >= 0) {
+        float cs, sn;
+        rope_rotation(p.rope.theta_pi[m], double(pos), &cs, &sn);
+        const float a = x[e], b = x[e + 1];
+        x[e] = a * cs - b * sn;
+        x[e + 1] = a * sn + b * cs;
+      }
+    }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void store_row(const float (&x)[kPer], int lane, int64_t row, uint8_t* codes, void* scales) {
+  if constexpr (FMT == DSV4KV_BF16) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(codes) + size_t(row) * kD + kPer * lane;
+#pragma unroll
+    for (int q = 0; q < kPer / 8; ++q)
+      *reinterpret_cast<uint4*>(dst + 8 * q) =
+          make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
+                     pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+  } else {
+    quantize_row<kPer, FMT>(x, lane, size_t(row), codes, scales);
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
+  x[0] = bf16lo(v.x); x[1] = bf16hi(v.x);
+  x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
+  x[4] = bf16lo(v.z); x[5] = bf16hi(v.z);
+  x[6] = bf16lo(v.w); x[7] = bf16hi(v.w);
+}
+
+// The state row of position q of token k's sequence (this lane's channels): a new token's or the raw ring's.
+__device__ __forceinline__ const uint16_t* state_row(const AppendParams& p, const Tok& k, int q, int lane) {
+  const int i = k.i - (k.pos - q);
+  if (i >= k.first) return p.s_new + size_t(i) * kD + kPer * lane;
+  const int R = p.window + p.k_taps;
+  return p.ring + (size_t(k.b) * R + q % R) * kD + kPer * lane;
+}
+
+__device__ __forceinline__ void add_tap(float (&acc)[kPer], const float (&w)[kPer], const uint4& a, const uint4& b) {
+  float x[kPer];
+  unpack8(a, x);
+  unpack8(b, x + 8);
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w[e], x[e], acc[e]);
+}
+__device__ __forceinline__ void load_weights(float (&w)[kPer], const float* src) {
+#pragma unroll
+  for (int q = 0; q < kPer / 4; ++q) {
+    const float4 v = *reinterpret_cast<const float4*>(src + 4 * q);
+    w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+  }
+}
+
+// Appends i to list[n ..] where `keep`, in thread order; returns the new length.  All threads call it.
+__device__ __forceinline__ int push_ordered(bool keep, int i, int32_t* list, int n, int* wcnt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned m = __ballot_sync(kFull, keep);
+  if (lane == 0) wcnt[warp] = __popc(m);
+  __syncthreads();
+  int before = n, all = n;
+#pragma unroll
+  for (int k = 0; k < kAppWarps; ++k) {
+    if (k < warp) before += wcnt[k];
+    all += wcnt[k];
+  }
+  if (keep) list[before + __popc(m & ((1u << lane) - 1u))] = i;
+  __syncthreads();
+  return all;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kAppThreads)
+    append_paged_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ int32_t rows[kMaxTokens], ents[kMaxTokens];
+  __shared__ int wcnt[kAppWarps];
+  extern __shared__ __align__(16) float red[];  // long entries: [warp][group][512]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i_first = blockIdx.x * p.per, i_end = min(p.tokens, i_first + p.per);
+  const int R = p.window + p.k_taps;
+  const double theta = p.rope.theta_pi[lane];
+  pdl_trigger();
+  pdl_wait();
+  // a token of the list: its sequence and the sequence's first new token
+  auto token = [&](int i) {
+    const int b = p.seq[i];
+    return Tok{i, b, int(p.pos[i]), p.cu[b]};
+  };
+  int n_rows = 0, n_ents = 0;
+  for (int i0 = i_first; i0 < i_end; i0 += kAppThreads) {
+    const int i = i0 + int(threadIdx.x);
+    bool row = false, ent = false;
+    if (i < i_end) {
+      const int b = p.seq[i];
+      if (b >= 0 && b < p.batch) {
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        const int64_t pos = p.pos[i];
+        const int ws = p.win_slot[i], cs = p.comp_slot[i];
+        if (i < c0 || i >= c1 || c0 < 0 || c1 > p.tokens || c1 - c0 > p.max_new || pos < i - c0 || pos >= (int64_t(1) << 31) - p.lookahead - 1) {
+          set_status(p.status, DSV4KV_DEV_BAD_LENGTH);
+        } else {
+          if (ws >= p.win_rows || cs >= p.comp_rows) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+          row = ((p.parts & kPartWindow) && ws >= 0 && ws < p.win_rows) || ((p.parts & kPartRing) && c1 - 1 - i < R);
+          ent = (p.parts & kPartEntries) && cs >= 0 && cs < p.comp_rows;
+          if (ent && pos + 1 + p.lookahead - p.window < p.stride) {  // no entry ends here
+            set_status(p.status, DSV4KV_DEV_BAD_LENGTH);
+            ent = false;
+          }
+        }
+      } else if (b != -1) {
+        set_status(p.status, DSV4KV_DEV_BAD_LENGTH);
+      }
+    }
+    n_rows = push_ordered(row, i, rows, n_rows, wcnt);
+    n_ents = push_ordered(ent, i, ents, n_ents, wcnt);
+  }
+  // ring and window rows
+  for (int r = warp; r < n_rows; r += kAppWarps) {
+    const Tok k = token(rows[r]);
+    const uint4* src = reinterpret_cast<const uint4*>(p.s_new + size_t(k.i) * kD + kPer * lane);
+    const uint4 v0 = src[0], v1 = src[1];
+    if ((p.parts & kPartRing) && p.cu[k.b + 1] - 1 - k.i < R) {
+      uint4* dst = reinterpret_cast<uint4*>(p.ring + (size_t(k.b) * R + k.pos % R) * kD + kPer * lane);
+      dst[0] = v0;
+      dst[1] = v1;
+    }
+    const int slot = p.win_slot[k.i];
+    if ((p.parts & kPartWindow) && slot >= 0 && slot < p.win_rows) {
+      float x[kPer];
+      unpack8(v0, x);
+      unpack8(v1, x + 8);
+      rotate_row(x, p, theta, k.pos, lane);
+      store_row<FMT>(x, lane, slot, p.win_codes, p.win_scales);
+    }
+  }
+  if (p.k_taps <= kLongTaps) {
+    for (int r = warp; r < n_ents; r += kAppWarps) {
+      const Tok k = token(ents[r]);
+      const int q0 = k.pos + 1 + p.lookahead - p.window - p.k_taps;
+      float acc[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+      for (int j = max(0, -q0); j < p.k_taps; ++j) {
+        const uint4* src = reinterpret_cast<const uint4*>(state_row(p, k, q0 + j, lane));
+        float w[kPer];
+        load_weights(w, p.w + size_t(j) * kD + kPer * lane);
+        add_tap(acc, w, src[0], src[1]);
+      }
+      rotate_row(acc, p, theta, q0 + p.k_taps - p.stride, lane);
+      store_row<FMT>(acc, lane, p.comp_slot[k.i], p.comp_codes, p.comp_scales);
+    }
+    return;
+  }
+  for (int r0 = 0; r0 < n_ents; r0 += kGroup) {
+    Tok k[kGroup];
+    int q0[kGroup];
+    float acc[kGroup][kPer];
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      k[g] = token(ents[min(r0 + g, n_ents - 1)]);
+      q0[g] = k[g].pos + 1 + p.lookahead - p.window - p.k_taps;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[g][e] = 0.f;
+    }
+    const int ng = min(kGroup, n_ents - r0);
+#pragma unroll 2
+    for (int j = warp; j < p.k_taps; j += kAppWarps) {
+      float w[kPer];
+      uint4 a[kGroup], b[kGroup];
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) {
+        a[g] = b[g] = make_uint4(0, 0, 0, 0);
+        if (g < ng && q0[g] + j >= 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(state_row(p, k[g], q0[g] + j, lane));
+          a[g] = src[0];
+          b[g] = src[1];
+        }
+      }
+      load_weights(w, p.w + size_t(j) * kD + kPer * lane);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) add_tap(acc[g], w, a[g], b[g]);
+    }
+    if (r0) __syncthreads();  // the previous group's sums are read
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      if (g >= ng) break;
+      float4* dst = reinterpret_cast<float4*>(red + (size_t(warp) * kGroup + g) * kD) + lane;
+#pragma unroll
+      for (int q = 0; q < kPer / 4; ++q)  // (element 16 lane + 4 q at [q][lane]: conflict-free)
+        dst[32 * q] = make_float4(acc[g][4 * q], acc[g][4 * q + 1], acc[g][4 * q + 2], acc[g][4 * q + 3]);
+    }
+    __syncthreads();
+    if (warp < ng) {
+      float x[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+      for (int ww = 0; ww < kAppWarps; ++ww) {
+        const float4* src = reinterpret_cast<const float4*>(red + (size_t(ww) * kGroup + warp) * kD) + lane;
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+          const float4 v = src[32 * q];
+          x[4 * q] += v.x; x[4 * q + 1] += v.y; x[4 * q + 2] += v.z; x[4 * q + 3] += v.w;
+        }
+      }
+      const Tok t = token(ents[r0 + warp]);
+      rotate_row(x, p, theta, t.pos + 1 + p.lookahead - p.window - p.stride, lane);
+      store_row<FMT>(x, lane, p.comp_slot[t.i], p.comp_codes, p.comp_scales);
+    }
+  }
+}
+
+template <int FMT>
+cudaError_t launch_append(const AppendParams& p, size_t smem, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  if (!done_on_device(ready)) {
+    const cudaError_t e = cudaFuncSetAttribute(append_paged_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(kAppWarps * kGroup * kD * sizeof(float)));
+    if (e != cudaSuccess) return e;
+    mark_done_on_device(ready);
+  }
+  const dim3 grid(unsigned((p.tokens + p.per - 1) / p.per));
+  return launch_pdl(append_paged_kernel<FMT>, grid, dim3(kAppThreads), smem, stream, p);
+}
+
+}  // namespace
+
+void rope_table_fill(RopeTable* r, int rope_dim, double rope_base) {
+  for (int m = 0; m < 256; ++m)
+    r->theta_pi[m] = m >= rope_dim / 2 ? 0.0 : pow(rope_base, -2.0 * double(m) / double(rope_dim)) / 3.141592653589793;
+}
+
+dsv4kv_status block_table_update_launch(const int64_t* t_old, const int64_t* t_new, int batch, int64_t t_max, int window,
+                                        int stride, int lookahead, int page_rows, int32_t* table, int table_stride,
+                                        int64_t pool_pages, int32_t* free_pages, int64_t free_cap,
+                                        const int64_t* free_count, int64_t* free_count_out, void* ws,
+                                        cudaStream_t stream) {
+  const TableParams p{t_old, t_new, batch, t_max, window, stride, lookahead, page_rows, table, table_stride,
+                      pool_pages, free_pages, free_cap, free_count, free_count_out, static_cast<uint32_t*>(ws)};
+  // a decode step changes at most a page or so per sequence; prompts bring up to table_stride of them
+  const int64_t most = int64_t(batch) * table_stride;
+  const int grid = int(std::max<int64_t>(1, std::min<int64_t>(sm_count(), most / (16 * kTabThreads))));
+  launch_pdl(block_table_kernel, dim3(grid), dim3(kTabThreads), size_t(2 * (batch + 1)) * sizeof(int32_t), stream, p);
+  return check_launch("block_table_kernel");
+}
+
+dsv4kv_status slot_map_launch(const int64_t* t_old, const int64_t* t_new, int batch, int64_t t_max, int window,
+                              int stride, int lookahead, const PageDesc& comp, const PageDesc& win, int capacity,
+                              int32_t* cu, int32_t* seq, int64_t* pos, int32_t* win_slot, int32_t* comp_slot, void* ws,
+                              cudaStream_t stream) {
+  const SlotParams p{t_old, t_new, batch, t_max, window, stride, lookahead, comp, win, capacity, cu, seq, pos,
+                     win_slot, comp_slot, static_cast<uint32_t*>(ws)};
+  const int per = kSlotThreads * kSlotPer;
+  const int grid = int(std::max<int64_t>(1, std::min<int64_t>(4 * sm_count(), (int64_t(capacity) + per - 1) / per)));
+  launch_pdl(slot_map_kernel, dim3(grid), dim3(kSlotThreads), size_t(batch + 1) * sizeof(int32_t), stream, p);
+  return check_launch("slot_map_kernel");
+}
+
+dsv4kv_status append_paged_launch(const void* s_new, const float* w, int batch, int tokens, const int32_t* cu,
+                                  const int32_t* seq, const int64_t* pos, const int32_t* win_slot,
+                                  const int32_t* comp_slot, int k_taps, int stride, int window, int lookahead,
+                                  int64_t max_new, int rope_dim, double rope_base, void* raw_ring,
+                                  const dsv4kv_cache& win, const dsv4kv_cache& comp, void* ws, cudaStream_t stream) {
+  AppendParams p;
+  p.s_new = static_cast<const uint16_t*>(s_new);
+  p.w = w;
+  p.batch = batch;
+  p.tokens = tokens;
+  p.cu = cu;
+  p.seq = seq;
+  p.pos = pos;
+  p.win_slot = win_slot;
+  p.comp_slot = comp_slot;
+  p.k_taps = k_taps;
+  p.stride = stride;
+  p.window = window;
+  p.lookahead = lookahead;
+  p.max_new = int(std::min<int64_t>(max_new, tokens));
+  p.rope_dim = rope_dim;
+  p.ring = static_cast<uint16_t*>(raw_ring);
+  p.win_codes = static_cast<uint8_t*>(const_cast<void*>(win.codes));
+  p.win_scales = const_cast<void*>(win.scales);
+  p.win_rows = window > 0 ? win.rows : 0;
+  p.comp_codes = static_cast<uint8_t*>(const_cast<void*>(comp.codes));
+  p.comp_scales = const_cast<void*>(comp.scales);
+  p.comp_rows = comp.rows;
+  p.status = static_cast<uint32_t*>(ws);
+  rope_table_fill(&p.rope, rope_dim, rope_base);
+  const bool lng = k_taps > kLongTaps;
+  // few tokens: spread them over the SMs; many: enough a CTA that four long entries share their weights
+  const int64_t spread = (int64_t(tokens) + 4 * sm_count() - 1) / (4 * sm_count());
+  p.per = int(std::max<int64_t>(1, std::min<int64_t>(spread, lng ? kMaxTokens : 128)));
+  const size_t smem = lng ? kAppWarps * kGroup * kD * sizeof(float) : 0;
+  const bool two = max_new > int64_t(lookahead) + 1;
+  for (int pass = 0; pass < (two ? 2 : 1); ++pass) {
+    p.parts = !two ? kPartEntries | kPartWindow | kPartRing : pass == 0 ? kPartEntries | kPartWindow : kPartRing;
+    cudaError_t e;
+    switch (comp.fmt) {
+      case DSV4KV_BF16: e = launch_append<DSV4KV_BF16>(p, smem, stream); break;
+      case DSV4KV_FP8_E4M3_ROW: e = launch_append<DSV4KV_FP8_E4M3_ROW>(p, smem, stream); break;
+      case DSV4KV_FP4_E2M1_G16: e = launch_append<DSV4KV_FP4_E2M1_G16>(p, smem, stream); break;
+      default: e = launch_append<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(p, smem, stream); break;
+    }
+    if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "append_paged_kernel: %s", cudaGetErrorString(e));
+    const dsv4kv_status st = check_launch("append_paged_kernel");
+    if (st != DSV4KV_OK) return st;
+  }
+  return DSV4KV_OK;
+}
+
+}  // namespace dsv4kv

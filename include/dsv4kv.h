@@ -57,6 +57,8 @@ typedef enum {
 #define DSV4KV_DEV_BAD_POOL 0x8u     /* a candidate pool was not ascending: ties may differ */
 #define DSV4KV_DEV_BAD_PAGE 0x10u    /* a block-table page number was outside the pool: its rows skipped */
 #define DSV4KV_DEV_BAD_LENGTH 0x20u  /* a sequence length was < 0 or > t_max: clamped into [0, t_max] */
+#define DSV4KV_DEV_NO_PAGES 0x40u    /* the free list ran out (or over): table entries -1, pages dropped */
+#define DSV4KV_DEV_BAD_TREE 0x80u    /* a parent was not an earlier node of its sequence: taken as a root */
 
 /* Cache row formats.
  *  DSV4KV_BF16:          codes = bf16 [B][rows][dim]; scales = NULL.
@@ -376,6 +378,162 @@ dsv4kv_status dsv4kv_dense_decode_paged(const void* q, const dsv4kv_paged_cache*
                                         const int64_t* t_seq, int64_t t_max, int32_t window, int32_t stride,
                                         float sm_scale, int32_t rope_dim, double rope_base, int32_t out_fp32,
                                         void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Block tables of a serving step.  [P1] hybrid KV cache manager paragraph: the
+ * caches are kept in blocks drawn from a shared block pool.
+ *
+ * Sequence b goes from t_old[b] to t_new[b] tokens (device int64 [batch]; 0 =
+ * not there: a new or a finished request).  A cache holds
+ *   rows(t) = max(0, floor((t + lookahead - window) / stride))  (stride >= 1)
+ *   rows(t) = min(t, window)                                    (stride == 0: a window cache)
+ * rows in pages(t) = ceil(rows(t) / page_rows) pages.  `free_pages` (device
+ * int32 [free_cap]) is a stack of *free_count free page numbers.
+ *   1. Sequences that shrink give back table[b][pages(t_new) .. pages(t_old)):
+ *      pushed in ascending (b, entry) order.  Their table entries keep the
+ *      old numbers (nothing reads past a sequence's rows).
+ *   2. Sequences that grow fill table[b][pages(t_old) .. pages(t_new)) in
+ *      ascending (b, entry) order, each entry popped from the end of the stack.
+ * *free_count_out is the count after both.  It may be free_count itself (a
+ * captured step that is replayed); with another word the call can be repeated
+ * on the same inputs with the same result.  A stack that runs out gives
+ * entries of -1 and one that would exceed free_cap drops pages, both with
+ * DSV4KV_DEV_NO_PAGES; a page number outside [0, pool_pages) sets
+ * DSV4KV_DEV_BAD_PAGE and is never handed out (the entry becomes -1); a
+ * length outside [0, t_max] or a count outside [0, free_cap] is clamped and
+ * sets DSV4KV_DEV_BAD_LENGTH.
+ * `lookahead` (0 <= lookahead <= window) also makes room for the entries that
+ * drafted tokens up to that many positions ahead attend to (dsv4kv_append_paged).
+ * Requirements: 0 <= batch <= 4096; t_max < 2^30; page_rows a positive
+ * multiple of 64; table_stride >= pages(t_max); pool_pages * page_rows < 2^31;
+ * batch * pages(t_max) < 2^31.
+ * Workspace: dsv4kv_paged_step_workspace_bytes.
+ * ------------------------------------------------------------------------ */
+size_t dsv4kv_paged_step_workspace_bytes(int32_t batch);
+
+dsv4kv_status dsv4kv_block_table_update(const int64_t* t_old, const int64_t* t_new, int32_t batch, int64_t t_max,
+                                        int32_t window, int32_t stride, int32_t lookahead, int32_t page_rows,
+                                        int32_t* table, int32_t table_stride, int64_t pool_pages,
+                                        int32_t* free_pages, int64_t free_cap, const int64_t* free_count,
+                                        int64_t* free_count_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Page numbers of a cache, without its rows. */
+typedef struct {
+  const int32_t* table;   /* device int32 [batch][table_stride] page numbers */
+  int32_t page_rows;      /* rows per page: a positive multiple of 64 */
+  int32_t table_stride;
+  int64_t pool_pages;
+} dsv4kv_page_table;
+
+/* ---------------------------------------------------------------------------
+ * Slot map of a serving step: where the new tokens of every sequence go.  The
+ * new tokens t_old[b] .. t_new[b]-1 of all sequences are packed in order of b
+ * (cu[b] = the first of sequence b, cu[batch] = their number).  For token i of
+ * sequence b at position p:
+ *   seq[i] = b, pos[i] = p;
+ *   win_slot[i]  = pool row of window row p % window if p >= t_new - window
+ *                  (the rows that stay), else -1;
+ *   comp_slot[i] = pool row of the entry that is written when p arrives,
+ *                  e = N(p + lookahead) if N(p + 1 + lookahead) > e, with
+ *                  N(t) = max(0, floor((t - window) / stride)), else -1.
+ * Outputs i >= cu[batch] are -1 up to `capacity`; tokens beyond the capacity
+ * are dropped (cu clamped to it) with DSV4KV_DEV_BAD_LENGTH.  A page number
+ * outside the pool gives a slot of -1 with DSV4KV_DEV_BAD_PAGE.  `win` may be
+ * NULL when window == 0, `comp` may be NULL (comp_slot all -1).
+ *   cu : int32 [batch + 1]; seq, win_slot, comp_slot : int32 [capacity];
+ *   pos : int64 [capacity]
+ * Requirements: 0 <= batch <= 4096; stride >= 1; 0 <= lookahead <= window <= 65536;
+ * t_max < 2^30; capacity < 2^31; seq, pos, win_slot and comp_slot 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+dsv4kv_status dsv4kv_slot_map(const int64_t* t_old, const int64_t* t_new, int32_t batch, int64_t t_max,
+                              int32_t window, int32_t stride, int32_t lookahead, const dsv4kv_page_table* comp,
+                              const dsv4kv_page_table* win, int64_t capacity, int32_t* cu, int32_t* seq,
+                              int64_t* pos, int32_t* win_slot, int32_t* comp_slot, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dsv4kv_append for paged caches of a ragged batch, any number of new tokens
+ * per sequence and any cache format.  The new states s_new (bf16
+ * [capacity][dim], packed) of a slot map's tokens update
+ *   raw_ring : bf16 [batch][window + k_taps][dim]; row p % (window + k_taps)
+ *              holds S[p] for the last window + k_taps positions;
+ *   win      : the row win_slot[i] = rope(S[p], p);
+ *   comp     : the row comp_slot[i] = the entry of dsv4kv_compress whose
+ *              number the slot map took, e = (p + 1 + lookahead - window) /
+ *              stride - 1, its taps s e + s - K + j < 0 zero;
+ * rows computed in fp32 and rounded once into the cache's format (quantised
+ * formats by the rule of dsv4kv_quantize).  With lookahead > 0 an entry is
+ * written that many positions before its block leaves the window: the entries
+ * that nodes drafted up to `lookahead` positions ahead attend to
+ * (dsv4kv_tree_decode_paged) are then in the cache; other calls never read
+ * them early.  Rows with a negative slot are not written; a slot outside the
+ * pool sets DSV4KV_DEV_BAD_PAGE, a token whose seq is outside [0, batch) (but
+ * not the -1 of the padding) or whose pos is negative DSV4KV_DEV_BAD_LENGTH;
+ * both are skipped.  A position is appended once: the rings hold what
+ * earlier calls appended.
+ *   max_new (host): no sequence has more new tokens.  With max_new <=
+ *   lookahead + 1 the call is one launch; otherwise a second one updates the
+ *   rings after the entries are read.
+ * cu, seq, pos, win_slot, comp_slot: as dsv4kv_slot_map writes them with the
+ * same window, stride and lookahead.  The two caches have one format; their
+ * tables are not read.  Requirements: dim == 512; rope_dim even, <= 512
+ * (64 with DSV4KV_FP8_E4M3_ROW_ROPE_BF16); 0 <= lookahead <= window; win may be
+ * NULL when window == 0; workspace as dsv4kv_block_table_update.
+ * ------------------------------------------------------------------------ */
+dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t batch, int64_t capacity,
+                                  const int32_t* cu, const int32_t* seq, const int64_t* pos, const int32_t* win_slot,
+                                  const int32_t* comp_slot, int32_t k_taps, int32_t stride, int32_t window,
+                                  int32_t lookahead, int64_t max_new, int32_t rope_dim, double rope_base,
+                                  void* raw_ring, const dsv4kv_paged_cache* win, const dsv4kv_paged_cache* comp,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode attention for trees of drafted tokens over paged caches of a ragged
+ * batch (verification of a speculative step).  Sequence b has t_seq[b]
+ * tokens in the caches and drafts m_b = cu[b+1] - cu[b] further ones, nodes of
+ * a tree (or of several): parent[cu[b] + i] is the number within the sequence
+ * (0 <= parent < i) of the node that node i follows, -1 when it follows the
+ * last cached token.  A node with d strict ancestors stands at position
+ * p = t_b + d.  It attends, as dsv4kv_{dense,sparse}_decode_paged would with
+ * its ancestors appended to the caches, in one softmax to
+ *   - the compressed entries [0, N(p)), N(p) = max(0, floor((p - window) /
+ *     stride)), or (idx) its own selected ones: the first min(k, N(p)) of its
+ *     row of idx (int32 [nodes][k], as dsv4kv_index_topk_paged writes them with
+ *     every node as a sequence of its own; any order, negative = none, an
+ *     index >= N(p) skipped and flagged DSV4KV_DEV_BAD_INDEX);
+ *   - the window rows of positions >= p - window (window row r holds the
+ *     position congruent to r modulo `window`, as dsv4kv_append and
+ *     dsv4kv_append_paged write them);
+ *   - the rows of its strict ancestors in `draft`,
+ * and its output's rotary pairs are rotated by -p * rope_base^(-2m/rope_dim).
+ * A node that sees no row gives zeros.  The entries [0, N(t_b + deepest d))
+ * have to be in the cache (dsv4kv_append_paged with a lookahead >= d).
+ *   q     : bf16 [nodes][heads][512], row cu[b] + i = node i of sequence b, rotated at its position
+ *   draft : cache of one sequence: row cu[b] + i = the (rotated) state of the node; format of comp
+ *   cu    : device int32 [batch + 1], ascending from 0; nodes (host) >= cu[batch]
+ *   parent: device int32 [nodes]
+ *   out   : bf16 or (out_fp32 != 0) float, [nodes][heads][512]; rows >= cu[batch] are left as they were
+ * max_nodes (host) must be >= every m_b, t_max >= every t_b.  A cu entry that
+ * descends, exceeds `nodes` or makes a tree larger than max_nodes is clamped and
+ * sets DSV4KV_DEV_BAD_LENGTH; a parent outside [-1, i) is taken as -1 and sets
+ * DSV4KV_DEV_BAD_TREE.  Rows no node of the call attends to are not read;
+ * infinities and NaN in rows that one node does not see stay out of its output.
+ * Requirements: dim == 512; 1 <= heads <= 128; 1 <= max_nodes <= 256;
+ * nodes * heads < 2^31; 1 <= batch <= 1024; the three caches of one format;
+ * 1 <= k <= 2048 with idx; stride >= 1; 0 <= window <= 65536; t_max < 2^30.
+ * ------------------------------------------------------------------------ */
+/* (k = 0: the dense form, idx NULL) */
+size_t dsv4kv_tree_decode_paged_workspace_bytes(int32_t batch, int32_t heads, int32_t dim, int32_t max_nodes,
+                                                int64_t nodes, int64_t t_max, int32_t window, int32_t stride,
+                                                int32_t k);
+
+dsv4kv_status dsv4kv_tree_decode_paged(const void* q, const dsv4kv_paged_cache* comp, const dsv4kv_paged_cache* win,
+                                       const dsv4kv_cache* draft, const int32_t* cu, const int32_t* parent,
+                                       const int32_t* idx, int32_t batch, int32_t heads, int64_t nodes,
+                                       int32_t max_nodes, const int64_t* t_seq, int64_t t_max, int32_t window,
+                                       int32_t stride, int32_t k, float sm_scale, int32_t rope_dim,
+                                       double rope_base, int32_t out_fp32, void* out, void* ws, size_t ws_bytes,
+                                       void* stream);
 
 /* Text of the last error on the calling host thread ("" if none). */
 const char* dsv4kv_last_error(void);

@@ -24,6 +24,9 @@ What it computes, and where each definition comes from (the pages are:
 * ``attention``  shared K/V decode attention over selected (or all) compressed
                  entries plus the 128-token window: [P1] "The sliding window",
                  "Shared key and value"; [P2] Steps 3, 5, 6.
+* ``serving``    block tables, slot maps and the append of a paged serving
+                 step, attention of drafted token trees: [P1] hybrid KV cache
+                 manager paragraph, "compressor-state blocks".
 * ``footprint``  closed-form cache sizes: [P1] opening summary, "To judge the
                  saving", hybrid cache manager paragraph.
 

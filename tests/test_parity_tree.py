@@ -1,0 +1,200 @@
+"""dsv4kv_tree_decode_paged against the float64 oracle: every format, head
+counts that do and do not divide a group of 64 query rows, lengths from none to
+long, trees of one node to many, cut and whole groups, selected entries."""
+import numpy as np
+import pytest
+import torch
+
+import compressed_sparse_kv_b200 as K
+from tests._serving import FORMATS, TreeCase
+
+pytestmark = pytest.mark.gpu
+
+RAGGED_T = [300, 0, 1, 5, 127, 128, 129, 9000]
+RAGGED_M = [4, 1, 3, 0, 6, 2, 9, 5]
+
+
+def both(case):
+    ws = case.workspace()
+    got = case.run(ws=ws)
+    case.check(got)
+    case.check(case.run(ws=ws, out_fp32=False), bf16=True)
+    assert K.workspace_status(ws) == 0
+    return got
+
+
+def test_one_node_one_short_sequence():
+    both(TreeCase(1, [130], [1], 64, K.BF16))
+
+
+def test_full_tiles_by_tma():
+    both(TreeCase(2, [128 * 400], [2], 64, K.BF16))        # 399 entries: three whole tiles and a tail
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_ragged_batch(fmt):
+    both(TreeCase(10 + fmt, RAGGED_T, RAGGED_M, 64, fmt, page=64, pad=3))
+
+
+@pytest.mark.parametrize("heads", [1, 5, 16, 20, 32, 65, 128])
+def test_head_counts(heads):
+    both(TreeCase(20 + heads, [700, 140, 33], [7, 3, 5], heads, K.BF16, page=128, stride=4))
+
+
+@pytest.mark.parametrize("fmt,heads", [(K.FP8_E4M3_ROW, 16), (K.FP4_E2M1_G16, 8), (K.FP8_E4M3_ROW_ROPE_BF16, 24)])
+def test_quantised_shared_groups(fmt, heads):
+    both(TreeCase(30 + fmt, [2000, 260], [9, 11], heads, fmt, page=256, stride=4))
+
+
+def test_a_long_chain_deeper_than_the_window():
+    chain = [list(range(-1, 39))]
+    both(TreeCase(41, [70], [40], 32, K.BF16, window=16, stride=4, parents=chain))
+
+
+def test_wide_tree_of_256_nodes():
+    both(TreeCase(42, [257, 90], [256, 17], 4, K.BF16, page=64, stride=128))
+
+
+@pytest.mark.parametrize("stride,window", [(1, 0), (3, 7), (128, 200)])
+def test_other_windows_and_strides(stride, window):
+    both(TreeCase(43 + stride, [411, 64, 3], [5, 4, 2], 24, K.BF16, window=window, stride=stride))
+
+
+def test_groups_cut_between_ctas():
+    """Few long groups: their tiles are spread over the SMs and merged."""
+    both(TreeCase(50, [40000, 9000, 200], [2, 1, 2], 64, K.BF16, stride=4, page=256))
+    both(TreeCase(51, [30000], [3], 48, K.FP8_E4M3_ROW, stride=4, page=128))
+
+
+def test_more_groups_than_sms():
+    both(TreeCase(52, [300, 513, 140], [90, 80, 70], 64, K.BF16, page=64))
+
+
+@pytest.mark.parametrize("fmt,heads,k", [(K.BF16, 64, 512), (K.FP8_E4M3_ROW, 16, 100), (K.FP4_E2M1_G16, 64, 64),
+                                         (K.FP8_E4M3_ROW_ROPE_BF16, 80, 130), (K.BF16, 3, 1)])
+def test_selected_entries(fmt, heads, k):
+    both(TreeCase(60 + fmt + k, [5000, 90, 640, 132], [4, 2, 6, 3], heads, fmt, stride=4, k=k))
+
+
+@pytest.mark.parametrize("fmt", [K.BF16, K.FP8_E4M3_ROW])
+def test_growing_scores_raise_the_maximum(fmt):
+    """Scores that grow along the rows pass the running maximum tile after tile."""
+    def grow(comp, win, draft):
+        for c in comp:
+            c *= np.linspace(0.1, 6, len(c))[:, None] if len(c) else 1.0
+    both(TreeCase(70 + fmt, [6000, 900], [3, 5], 32, fmt, stride=4, q_scale=3.0, edit=grow))
+
+
+def test_repeated_calls_and_workspace_reuse_are_bitwise_equal():
+    a, b = TreeCase(80, [20000], [2], 64, K.BF16, stride=4), TreeCase(81, [300, 70], [3, 4], 16, K.BF16)
+    ws = K.new_workspace(max(a.workspace().numel(), b.workspace().numel()))
+    first = a.run(ws=ws).clone()
+    other = b.run(ws=ws).clone()
+    assert torch.equal(a.run(ws=ws), first) and torch.equal(b.run(ws=ws), other)
+
+
+def test_rows_behind_the_last_sequence_are_left():
+    c = TreeCase(82, [200, 50], [3, 2], 16, K.BF16, pad=6)
+    out = torch.full((c.rows, 16, 512), 7.0, device="cuda")
+    c.run(out=out)
+    c.check(out)
+    assert torch.all(out[c.total:] == 7.0)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("heads", [64, 8])
+def test_bad_rows_stay_with_the_nodes_that_see_them(heads, bad):
+    """A sibling's drafted row, a window row that deeper nodes have left behind and an entry that shallow ones do not
+    see yet hold an infinity or NaN: only the nodes that attend to them are affected."""
+    parents = [[-1, 0, 0, 2, 3]]                            # node 1 is nobody's ancestor; 4 sees 0, 2, 3
+    clean = TreeCase(90, [256 + 126], [5], heads, K.BF16, parents=parents)
+
+    def spoil(comp, win, draft):
+        assert len(comp[0]) == 2                            # entry 1 is seen from depth 2 on
+        comp[0][1, 5] = bad
+        draft[0][1, 7] = bad
+        win[0][(382 - 128) % 128, 9] = bad                  # position 254: seen by depth 0 only
+    c = TreeCase(90, [256 + 126], [5], heads, K.BF16, parents=parents, edit=spoil)
+    got, want = c.run(), clean.run()
+    for j, clear in enumerate([False, True, True, False, False]):   # depths 0, 1, 1, 2, 3
+        if clear:
+            assert torch.equal(got[j], want[j])
+        else:
+            assert not torch.isfinite(got[j]).all()
+
+
+def test_a_bad_query_stays_in_its_row():
+    c = TreeCase(91, [300], [4], 16, K.BF16)
+    want = c.run().clone()
+    c.q[1, 3, 11] = float("nan")
+    got = c.run()
+    assert torch.isnan(got[1, 3]).all()
+    got[1, 3] = want[1, 3]
+    assert torch.equal(got, want)
+
+
+def test_bad_inputs_are_flagged_not_faulted():
+    c = TreeCase(92, [2000, 600], [4, 3], 16, K.BF16, stride=4)
+
+    def flags(**kw):
+        d = TreeCase.__new__(TreeCase)
+        d.__dict__.update(c.__dict__, **kw)
+        ws = d.workspace()
+        out = d.run(ws=ws)
+        assert torch.isfinite(out[:c.total]).all() or "cu_d" in kw
+        return K.workspace_status(ws)
+
+    assert flags(parent=torch.tensor([0, 0, 9, -3, 2, 0, 1], dtype=torch.int32, device="cuda")) == K.DEV_BAD_TREE
+    assert flags(t_seq=torch.tensor([2000, -4], device="cuda")) == K.DEV_BAD_LENGTH
+    assert flags(cu_d=torch.tensor([0, 5, 3], dtype=torch.int32, device="cuda")) & K.DEV_BAD_LENGTH
+    assert flags(cu_d=torch.tensor([-2, 4, 90], dtype=torch.int32, device="cuda")) & K.DEV_BAD_LENGTH
+    tab = c.comp.table.clone()
+    tab[0, 1], tab[0, 2] = -1, c.comp.pool_pages
+    assert flags(comp=K.PagedCache(c.fmt, c.comp.codes, tab, c.comp.page_rows)) == K.DEV_BAD_PAGE
+    wtab = c.win.table.clone()
+    wtab[1, 0] = 1 << 30
+    assert flags(win=K.PagedCache(c.fmt, c.win.codes, wtab, c.win.page_rows)) == K.DEV_BAD_PAGE
+    s = TreeCase(93, [2000], [2], 16, K.BF16, stride=4, k=8)
+    s.idx[0, 3] = 100000
+    ws = s.workspace()
+    assert torch.isfinite(s.run(ws=ws)).all() and K.workspace_status(ws) == K.DEV_BAD_INDEX
+
+
+def test_captured_and_replayed_with_new_lengths():
+    """One graph for a serving loop: lengths, trees and queries change between replays."""
+    a = TreeCase(100, [900, 300], [5, 4], 16, K.BF16, stride=4)
+    b = TreeCase(101, [850, 120], [4, 5], 16, K.BF16, stride=4)
+    ws, out = a.workspace(), torch.empty(9, 16, 512, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.run(ws=ws, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.run(ws=ws, out=out)
+    g.replay()
+    a.check(out)
+    # b's inputs moved into a's buffers
+    rows = b.comp.codes.shape[0], b.win.codes.shape[0]
+    assert rows[0] <= a.comp.codes.shape[0] and rows[1] <= a.win.codes.shape[0]
+    a.comp.codes[:rows[0]], a.win.codes[:rows[1]] = b.comp.codes, b.win.codes
+    a.comp.table.fill_(-1)
+    a.comp.table[:, :b.comp.table.shape[1]] = b.comp.table
+    a.win.table.copy_(b.win.table)
+    a.draft.codes.copy_(b.draft.codes)
+    for x, y in ((a.q, b.q), (a.cu_d, b.cu_d), (a.parent, b.parent), (a.t_seq, b.t_seq)):
+        x.copy_(y)
+    g.replay()
+    b.check(out)
+
+
+def test_two_streams_at_once():
+    a, b = TreeCase(110, [20000], [3], 64, K.BF16, stride=4), TreeCase(111, [16000], [2], 64, K.FP8_E4M3_ROW, stride=4)
+    want = a.run().clone(), b.run().clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        got = a.run(stream=s[0]), b.run(stream=s[1])
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
