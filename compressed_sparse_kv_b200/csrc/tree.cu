@@ -18,11 +18,11 @@
 // end to end and cut into equal runs, a group cut by a run boundary leaving
 // fp32 partial sums (O, m, l) that tree_combine merges with log-sum-exp weights.
 //
-// A tile (16 warps).  Shared memory holds the queries (64 KB), one tile (128 KB:
+// A tile (22 warps).  Shared memory holds the queries (64 KB), one tile (128 KB:
 // 8 slabs of 64 channels x 128 rows, 128-byte swizzle) and the weights (16 KB).
 //   * S^T = R . Q^T: M = 128 rows, N = 64 queries, 32 K-steps (one tcgen05.mma
 //     each), into TMEM (lane = row, column = query);
-//   * 8 softmax warps, one row and 32 queries a thread: the weights
+//   * 16 softmax warps, one row and 16 queries a thread: the weights
 //     2^(x - m_j) against a running maximum m_j that is raised only when some
 //     score passes it by 2^8 (one vote a tile; the column maxima are reduced
 //     over the rows only then), rounded to 16 bits and stored row by row, which
@@ -31,7 +31,7 @@
 //   * O^T += R^T . P^T: four blocks of M = 128 channels, N = 64, 8 K-steps, from
 //     the SAME slabs.  A block's commit frees its two slabs, so the next tile
 //     loads behind the products (warp 0 by TMA for whole bf16 tiles, warps
-//     12-15 otherwise: 16-byte cp.async, or dequantisation to f16 as in the
+//     2-5 otherwise: 16-byte cp.async, or dequantisation to f16 as in the
 //     decode kernel).
 // Rows that no node of the batch may read are zero-filled, not loaded.  A loaded
 // row that some query of the group does not see has weight 0 for it; if it
@@ -58,12 +58,16 @@ constexpr int kQSlab = kQ * 128;               // 8 KB
 constexpr int kQBytes = kSlabs * kQSlab;       // 64 KB
 constexpr int kPBytes = kRows * 128;           // 64 weights of 16 bits per row
 constexpr int kParts = 4;                      // slab pairs = 128-channel blocks
-constexpr int kThreads = 512;
+constexpr int kThreads = 704;
+constexpr int kLoad0 = 2, kSoft0 = 6;  // first loader warp (4 of them), first softmax warp (16)
+constexpr int kSoftThreads = 512;
+constexpr int kCols = 16;          // queries a softmax thread
 constexpr int kMaxBatch = 1024;
 constexpr int kMaxNodes = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;    // O^T: 4 channel blocks x 64 queries
 constexpr uint32_t kColS = 256;  // S^T: 64 columns
+constexpr float kNoMax = -1e30f;  // a maximum that nothing has reached yet
 constexpr float kRaise = 8.0f;   // log2 units a score may pass the running maximum by
 constexpr int kSplitCost = 3;    // tiles that a cut group's partial sums and merge cost (see split rule)
 
@@ -111,8 +115,7 @@ struct Seg {  // the part of a group that a CTA works on
   int row0, rows;           // first query row, query rows
   int node0, n_nodes;       // nodes of the group (numbers within the sequence)
   int n, full, rem;         // compressed rows listed, whole tiles of them, rows in the tail
-  int n_min, p_max;         // least entry count / greatest position of the group's nodes
-  int more;
+  int n_min;                // least entry count of the group's nodes
 };
 
 struct __align__(16) Ctl {
@@ -120,21 +123,19 @@ struct __align__(16) Ctl {
   uint64_t full[kParts], empty[kParts];
   uint32_t tmem_base;
   volatile int abort;
-  int dmax;
-  int start_b, start_off;  // (split) first sequence and unit offset of this CTA
-  long long units;
-  int max_tiles;
-  int whole;
-  Seg seg;
+  int dmax, n_min;
+  int b, g, t0;       // the next part to work on
+  int whole, share, units;
   uint32_t ok[2][4];  // rows of a tile that the loader warps brought, one word a warp
   float scale[2][kRows];
-  float m[kQ], alpha[kQ], lsum[4][kQ], wmax[4][kQ];
+  __align__(16) float m[kQ];
+  __align__(16) float alpha[kQ];
+  float part[4][kQ];  // column maxima / sums of the four row quarters
+  int col_pos[kQ];          // position of a column's node
   uint64_t colmask[kQ];     // columns of the group's node j
   int node_n[kQ], node_p[kQ];
   uint32_t anc[kQ][kMaxNodes / 32];
   int16_t parent[kMaxNodes];
-  int16_t depth[kMaxNodes];
-  long long wsum[kThreads / 32];
   int gpre[kMaxBatch + 1];  // groups before sequence b
   int tiles[kMaxBatch];     // tiles of each group of sequence b
 };
@@ -177,22 +178,45 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   if (lane == 0) ok = wait_bar(bar, parity, abort);
   return __shfl_sync(kFull, ok, 0);
 }
-__device__ __forceinline__ bool soft_or(bool pred) {  // over the 256 softmax threads
+__device__ __forceinline__ bool soft_or(bool pred) {  // over the softmax threads
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.cta.red.or.pred po, 1, 256, pi;\n\tselp.u32 "
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.cta.red.or.pred po, 1, 512, pi;\n\tselp.u32 "
       "%0, 1, 0, po;\n\t}"
       : "=r"(r)
       : "r"(uint32_t(pred))
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_approx(float x) {  // max relative error ~2^-22, far below the weights' 16 bits
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Reduces v[j] (j < 16) over the 32 lanes: the lane gets column col_of(lane)'s result.  Each step sends half of
+// the columns to the lane that keeps them: 16 shuffles instead of 80.
+__device__ __forceinline__ int col_of(int lane) {
+  return ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
+}
+template <class Op>
+__device__ __forceinline__ float reduce_cols(float (&v)[kCols], int lane, Op op) {
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    const bool up = (lane & (2 * h)) != 0;
+#pragma unroll
+    for (int j = 0; j < h; ++j) {
+      const float keep = up ? v[j + h] : v[j], send = up ? v[j] : v[j + h];
+      v[j] = op(keep, __shfl_xor_sync(kFull, send, 2 * h));
+    }
+  }
+  return op(v[0], __shfl_xor_sync(kFull, v[0], 1));
+}
+
+__device__ __noinline__ void rotation(double theta_pi, int pos, float* cs, float* sn) {
+  rope_rotation(theta_pi, -double(pos), cs, sn);
 }
 
 __device__ __forceinline__ int entries(int t, int window, int stride) {
@@ -315,43 +339,41 @@ __device__ __forceinline__ void put_fp8x16(uint8_t* tile, int r, int ch, const u
   *reinterpret_cast<uint4*>(cell(tile, r, ch + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-// The warp's rows of slab pair `sp` in registers (fetch), then as f16 in the tile (put).
+// A part of the warp's rows in registers (fetch), then as f16 in the tile (put).  Parts 0 .. 3 are the slab pairs
+// (128 channels); with bf16 rotary channels pair 3 holds 64 fp8 channels and part 4 the 64 rotary ones.
 template <int FMT>
 struct QuantPart {
+  static constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16;
+  static constexpr int kCount = kRope ? 5 : 4;
   static constexpr int kN = FMT == DSV4KV_FP4_E2M1_G16 ? 4 : 8;
   uint4 raw[kN];
-  uint4 rot[FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16 ? kN : 1];
   uint32_t sc[FMT == DSV4KV_FP4_E2M1_G16 ? kN : 1];
 
   // my: this lane's row (codes; null: none), mysc: its fp4 scales
-  __device__ __forceinline__ void fetch(const uint8_t* my, const uint8_t* mysc, int sp, int lane) {
-    if constexpr (FMT == DSV4KV_FP4_E2M1_G16) {  // 4 lanes a row: 32 channels, 16 bytes of codes, 2 scales each
+  __device__ __forceinline__ void fetch(const uint8_t* my, const uint8_t* mysc, int part, int lane) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
+    for (int i = 0; i < kN; ++i) {
+      if constexpr (FMT == DSV4KV_FP4_E2M1_G16) {  // 4 lanes a row: 32 channels, 16 bytes of codes, 2 scales each
         const int r = 8 * i + (lane >> 2), c = lane & 3;
         const uint8_t* row = reinterpret_cast<const uint8_t*>(shfl_ptr(my, r));
         const uint8_t* srow = reinterpret_cast<const uint8_t*>(shfl_ptr(mysc, r));
-        raw[i] = row ? ld_stream_v4(row + 64 * sp + 16 * c) : make_uint4(0, 0, 0, 0);
-        sc[i] = row ? *reinterpret_cast<const uint16_t*>(srow + 8 * sp + 2 * c) : 0u;
-      }
-    } else {  // 8 lanes a row: 16 channels each
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
+        raw[i] = row ? ld_stream_v4(row + 64 * part + 16 * c) : make_uint4(0, 0, 0, 0);
+        sc[i] = row ? *reinterpret_cast<const uint16_t*>(srow + 8 * part + 2 * c) : 0u;
+      } else {  // 8 lanes a row: 16 bytes each
         const int r = 4 * i + (lane >> 3), c = lane & 7;
         const uint8_t* row = reinterpret_cast<const uint8_t*>(shfl_ptr(my, r));
-        const bool body = FMT == DSV4KV_FP8_E4M3_ROW || sp < 3 || c < 4;  // 448 fp8 channels end inside pair 3
-        raw[i] = row && body ? ld_stream_v4(row + 128 * sp + 16 * c) : make_uint4(0, 0, 0, 0);
-        if constexpr (FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16)
-          if (sp == 3) rot[i] = row ? ld_stream_v4(row + (kDim - 64) + 16 * c) : make_uint4(0, 0, 0, 0);
+        const bool in = !kRope || part != 3 || c < 4;
+        raw[i] = row && in ? ld_stream_v4(row + (kRope && part == 4 ? kDim - 64 : 128 * part) + 16 * c)
+                           : make_uint4(0, 0, 0, 0);
       }
     }
   }
   // my_inv: 1 / (this lane's row's scale)
-  __device__ __forceinline__ void put(uint8_t* tile, int lw, int sp, float my_inv, int lane) const {
-    if constexpr (FMT == DSV4KV_FP4_E2M1_G16) {
+  __device__ __forceinline__ void put(uint8_t* tile, int lw, int part, float my_inv, int lane) const {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const int r = 32 * lw + 8 * i + (lane >> 2), ch = 128 * sp + 32 * (lane & 3);
+    for (int i = 0; i < kN; ++i) {
+      if constexpr (FMT == DSV4KV_FP4_E2M1_G16) {
+        const int r = 32 * lw + 8 * i + (lane >> 2), ch = 128 * part + 32 * (lane & 3);
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -362,21 +384,17 @@ struct QuantPart {
           for (int j = 0; j < 4; ++j) h[j] = hmul2(e2m1x2_to_f16x2((w[e] >> (8 * j)) & 0xffu), s2);
           *reinterpret_cast<uint4*>(cell(tile, r, ch + 8 * e)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
+      } else {
         const int rl = 4 * i + (lane >> 3), r = 32 * lw + rl, c = lane & 7;
-        if (FMT == DSV4KV_FP8_E4M3_ROW || sp < 3 || c < 4) put_fp8x16(tile, r, 128 * sp + 16 * c, raw[i]);
-        if constexpr (FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16) {
+        if (kRope && part == 4) {  // rotary channels as f16(value / scale): the row's scale is in the weights
           const float inv = __shfl_sync(kFull, my_inv, rl);
-          if (sp == 3) {  // rotary channels as f16(value / scale): the row's scale is in the weights
-            const uint32_t w[4] = {rot[i].x, rot[i].y, rot[i].z, rot[i].w};
-            uint32_t h[4];
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t h[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = f32x2_to_f16x2_sat(bf16lo(w[e]) * inv, bf16hi(w[e]) * inv);
-            *reinterpret_cast<uint4*>(cell(tile, r, kDim - 64 + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
+          for (int e = 0; e < 4; ++e) h[e] = f32x2_to_f16x2_sat(bf16lo(w[e]) * inv, bf16hi(w[e]) * inv);
+          *reinterpret_cast<uint4*>(cell(tile, r, kDim - 64 + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+        } else if (!kRope || part != 3 || c < 4) {
+          put_fp8x16(tile, r, 128 * part + 16 * c, raw[i]);
         }
       }
     }
@@ -388,6 +406,33 @@ __host__ __device__ constexpr int row_bytes(int fmt) {
          : fmt == DSV4KV_FP8_E4M3_ROW ? kDim
          : fmt == DSV4KV_FP4_E2M1_G16 ? kDim / 2
                                       : kDim + 64;
+}
+
+// A row hidden from some query (`hid`: columns) whose masked scores are not finite: if the row itself is not finite it
+// is zeroed in the tile, so that its zero weights add zeros.  (A query that is not finite itself says nothing.)
+template <bool kF16>
+__device__ __noinline__ void zero_bad_row(uint8_t* tile, int r, Ctl* ctl, int c) {
+  for (int sp = 0; sp < kParts; ++sp) wait_bar(&ctl->full[sp], c & 1, &ctl->abort);  // (complete: orders the row's loads)
+  const uint32_t e = kF16 ? 0x7c00u : 0x7f80u;
+  bool bad = false;
+#pragma unroll 1
+  for (int ch = 0; ch < kDim; ch += 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(cell(tile, r, ch));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad |= (w[k] & e) == e || ((w[k] >> 16) & e) == e;
+  }
+  if (!bad) return;
+#pragma unroll 1
+  for (int ch = 0; ch < kDim; ch += 8) *reinterpret_cast<uint4*>(cell(tile, r, ch)) = make_uint4(0, 0, 0, 0);
+}
+template <bool kF16>
+__device__ __forceinline__ void hide_bad_row(const uint32_t (&raw)[kCols], uint32_t hid, uint8_t* tile, int r, Ctl* ctl,
+                                             int c) {
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) odd |= ((hid >> j) & 1u) && (raw[j] & 0x7f800000u) == 0x7f800000u;
+  if (odd) zero_bad_row<kF16>(tile, r, ctl, c);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -410,208 +455,171 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->s_full, 1);
-    mbar_init(&ctl->p_full, 8);
+    mbar_init(&ctl->p_full, kSoftThreads / 32);
     mbar_init(&ctl->o_done, 1);
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&ctl->full[i], 5);  // warp 0 and the four loader warps, every tile
       mbar_init(&ctl->empty[i], 1);
     }
     ctl->abort = 0;
-    ctl->units = 0;
-    ctl->max_tiles = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (tid == 32) {
+  if (tid == 64) {
     prefetch_tmap(&tm_q);
     if (!C::kQuant) prefetch_tmap(&tm_comp);
   }
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
   pdl_wait();
 
-  // ---- the batch: groups, tiles, and which part of them is this CTA's
-  {
-    int g_sum = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-      const int b = b0 + tid;
-      int groups = 0, tiles = 0;
-      if (b < p.batch) {
-        int c0, m;
-        uint32_t* st = cta == 0 ? p.status : nullptr;
-        seq_nodes(p, b, &c0, &m, st);
-        const int t = seq_len(p, b, st);
-        groups = groups_of(p, m);
-        tiles = m > 0 ? tiles_of(p, entries(t + m - 1, p.window, p.stride), min(t, p.window), m) : 0;
-        ctl->tiles[b] = tiles;
-        if (groups > 0) atomicMax(&ctl->max_tiles, tiles);
-      }
-      // groups before b in this pass (low half) and units (high: kept apart, they may pass 32 bits)
-      int x = groups;
+  // ---- the batch: groups and tiles of every sequence, then which part of them is this CTA's
+  for (int b = tid; b < p.batch; b += kThreads) {
+    int c0, m;
+    uint32_t* st = cta == 0 ? p.status : nullptr;
+    seq_nodes(p, b, &c0, &m, st);
+    const int t = seq_len(p, b, st);
+    ctl->gpre[b + 1] = groups_of(p, m);
+    ctl->tiles[b] = m > 0 ? tiles_of(p, entries(t + m - 1, p.window, p.stride), min(t, p.window), m) : 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int g = 0, u = 0, most = 0;  // groups, units (tiles of all groups: < 2^31), most tiles of a group
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const int n = b < p.batch ? ctl->gpre[b + 1] : 0, tl = b < p.batch ? ctl->tiles[b] : 0;
+      int x = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFull, x, o);
         if (lane >= o) x += y;
       }
-      if (lane == 31) ctl->wsum[warp] = x;
-      __syncthreads();
-      int before = g_sum, all = g_sum;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += int(ctl->wsum[i]);
-        all += int(ctl->wsum[i]);
-      }
-      if (b < p.batch) ctl->gpre[b] = before + x - groups;
-      g_sum = all;
-      __syncthreads();
+      if (b < p.batch) ctl->gpre[b + 1] = g + x;
+      g += __shfl_sync(kFull, x, 31);
+      u += __reduce_add_sync(kFull, unsigned(n) * unsigned(tl));
+      most = max(most, __reduce_max_sync(kFull, n > 0 ? tl : 0));
     }
-    if (tid == 0) ctl->gpre[p.batch] = g_sum;
-    // units: tiles of all groups; then the sequence in which this CTA's run starts
-    long long carry = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-      carry = 0;
-      __syncthreads();
-      const int G = ctl->gpre[p.batch];
-      const long long U = pass ? ctl->units : 0;
-      const long long share = pass ? max(1ll, (U + P - 1) / P) : 0, want = share * cta;
-      for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        const long long v =
-            b < p.batch ? (long long)(ctl->gpre[b + 1] - ctl->gpre[b]) * ctl->tiles[b] : 0;
-        long long x = v;
+    if (lane == 0) ctl->gpre[0] = 0;
+    __syncwarp();
+    // whole groups when that takes no longer than equal runs of tiles plus a merge
+    const int share = max(1, (u + P - 1) / P), rounds = (g + P - 1) / P;
+    const bool whole = (long long)rounds * most <= share + kSplitCost;
+    if (lane == 0) {
+      ctl->whole = whole;
+      ctl->share = share;
+      ctl->units = u;
+    }
+    const unsigned want = whole ? unsigned(cta) : unsigned(share) * unsigned(cta);
+    unsigned at = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const unsigned tl = b < p.batch ? ctl->tiles[b] : 0;
+      const unsigned v = b < p.batch ? unsigned(ctl->gpre[b + 1] - ctl->gpre[b]) * (whole ? 1u : tl) : 0u;
+      unsigned x = v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(kFull, x, o);
-          if (lane >= o) x += y;
-        }
-        if (lane == 31) ctl->wsum[warp] = x;
-        __syncthreads();
-        long long before = carry, all = carry;
-        for (int i = 0; i < kThreads / 32; ++i) {
-          if (i < warp) before += ctl->wsum[i];
-          all += ctl->wsum[i];
-        }
-        const long long ex = before + x - v;
-        if (pass && v > 0 && want >= ex && want < ex + v) {
-          const long long off = want - ex;
-          ctl->seg.b = b;
-          ctl->seg.g = int(off / ctl->tiles[b]);
-          ctl->seg.t0 = int(off % ctl->tiles[b]);
-        }
-        carry = all;
-        __syncthreads();
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
       }
-      if (!pass && tid == 0) {
-        ctl->units = carry;
-        // whole groups when that takes no longer than equal runs plus a merge
-        const long long whole = (long long)((G + P - 1) / P) * ctl->max_tiles;
-        ctl->whole = whole <= (carry + P - 1) / P + kSplitCost;
+      const unsigned ex = at + x - v;
+      if (want >= ex && want - ex < v) {
+        const unsigned off = want - ex;
+        ctl->b = b;
+        ctl->g = whole ? off : off / tl;
+        ctl->t0 = whole ? 0 : off % tl;
       }
+      at += __shfl_sync(kFull, x, 31);
     }
   }
-  const long long U = ctl->units;
-  const long long share = max(1ll, (U + P - 1) / P);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
   const bool whole = ctl->whole != 0;
   const int G = ctl->gpre[p.batch];
-  long long left = max(0ll, min(share, U - share * cta));  // units of this CTA's run (equal runs)
-  if (whole) {
-    // sequence of group `cta`
-    for (int b = tid; b < p.batch; b += kThreads)
-      if (ctl->gpre[b] <= cta && cta < ctl->gpre[b + 1]) {
-        ctl->seg.b = b;
-        ctl->seg.g = cta - ctl->gpre[b];
-        ctl->seg.t0 = 0;
-      }
-  }
-  int g_next = cta;  // (whole groups) the flattened group to take next
+  // (equal runs) tiles of this CTA's run; (whole groups) the flattened group to take next
+  int left = int(max(0ll, min((long long)ctl->share, ctl->units - (long long)ctl->share * cta)));
+  int g_next = cta;
   if (tid < 2) p.rec[2 * cta + tid].valid = 0;
 
   int cnt = 0, segs = 0;  // tiles and groups worked on so far: the barriers' phases
   while (whole ? g_next < G : left > 0) {
-    __syncthreads();  // (the previous group's roles are done; seg.{b, g, t0} are set)
-    if (tid == 0) {
-      Seg& s = ctl->seg;
-      s.tiles = ctl->tiles[s.b];
-      s.t1 = whole ? s.tiles : int(min((long long)s.tiles, s.t0 + left));
-      s.t = seq_len(p, s.b, nullptr);
-      seq_nodes(p, s.b, &s.c0, &s.m, nullptr);
-      s.w = min(s.t, p.window);
-      if (p.idx) {
-        const int gpn = (p.heads + kQ - 1) / kQ, h0 = (s.g % gpn) * kQ;
-        s.node0 = s.g / gpn;
-        s.n_nodes = 1;
-        s.row0 = (s.c0 + s.node0) * p.heads + h0;
-        s.rows = min(kQ, p.heads - h0);
-      } else {
-        const int f = kQ * s.g;
-        s.rows = min(kQ, s.m * p.heads - f);
-        s.node0 = f / p.heads;
-        s.n_nodes = (f + s.rows - 1) / p.heads - s.node0 + 1;
-        s.row0 = s.c0 * p.heads + f;
-      }
-      s.n_min = 0x7fffffff;
-      s.p_max = 0;
+    // ---- the group: its rows, its nodes and their ancestors
+    Seg s;
+    s.b = ctl->b;
+    s.g = ctl->g;
+    s.t0 = ctl->t0;
+    s.tiles = ctl->tiles[s.b];
+    s.t1 = whole ? s.tiles : min(s.tiles, s.t0 + left);
+    seq_nodes(p, s.b, &s.c0, &s.m, nullptr);
+    s.t = seq_len(p, s.b, nullptr);
+    s.w = min(s.t, p.window);
+    if (p.idx) {
+      const int gpn = (p.heads + kQ - 1) / kQ, h0 = (s.g % gpn) * kQ;
+      s.node0 = s.g / gpn;
+      s.n_nodes = 1;
+      s.row0 = (s.c0 + s.node0) * p.heads + h0;
+      s.rows = min(kQ, p.heads - h0);
+    } else {
+      const int f = kQ * s.g;
+      s.rows = min(kQ, s.m * p.heads - f);
+      s.node0 = f / p.heads;
+      s.n_nodes = (f + s.rows - 1) / p.heads - s.node0 + 1;
+      s.row0 = s.c0 * p.heads + f;
+    }
+    if (tid == 0) {  // the queries (the previous group's products have read theirs)
+      mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
+#pragma unroll 1
+      for (int c = 0; c < kSlabs; ++c) tma_load_2d(sQ + c * kQSlab, &tm_q, &ctl->q_full, 64 * c, s.row0);
+    }
+    if (tid == kThreads - 1) {
       ctl->dmax = 0;
+      ctl->n_min = 0x7fffffff;
+    }
+    if (tid < s.m) {  // (at most 256 nodes)
+      int par = p.parent[s.c0 + tid];
+      if (par < -1 || par >= tid) {
+        set_status(p.status, DSV4KV_DEV_BAD_TREE);
+        par = -1;
+      }
+      ctl->parent[tid] = int16_t(par);
+    }
+    for (int i = tid; i < kQ * (kMaxNodes / 32); i += kThreads) (&ctl->anc[0][0])[i] = 0;
+    if (tid < kQ) ctl->m[tid] = kNoMax;
+    __syncthreads();
+    if (tid < s.m) {
+      int d = 0;
+      const int gj = tid - s.node0;
+      const bool mine = gj >= 0 && gj < s.n_nodes;
+      for (int j = ctl->parent[tid]; j >= 0; j = ctl->parent[j]) {
+        ++d;
+        if (mine) ctl->anc[gj][j >> 5] |= 1u << (j & 31);
+      }
+      atomicMax(&ctl->dmax, d);
+      if (mine) {
+        const int pos = s.t + d, n = entries(pos, p.window, p.stride);
+        ctl->node_p[gj] = pos;
+        ctl->node_n[gj] = n;
+        atomicMin(&ctl->n_min, n);
+        // its columns: query rows tid * heads .. + heads of the sequence, within the group
+        const int lo = p.idx ? 0 : max(0, tid * p.heads - kQ * s.g);
+        const int hi = p.idx ? s.rows : min(s.rows, (tid + 1) * p.heads - kQ * s.g);
+        ctl->colmask[gj] = (hi >= 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
+      }
     }
     __syncthreads();
-    // the queries (the previous group's products have read theirs)
-    if (tid == 0) {
-      mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
-      for (int c = 0; c < kSlabs; ++c) tma_load_2d(sQ + c * kQSlab, &tm_q, &ctl->q_full, 64 * c, ctl->seg.row0);
-    }
-    {  // the tree: parents, depths, the ancestors of the group's nodes
-      const Seg& s = ctl->seg;
-      for (int i = tid; i < s.m; i += kThreads) {
-        int par = p.parent[s.c0 + i];
-        if (par < -1 || par >= i) {
-          set_status(p.status, DSV4KV_DEV_BAD_TREE);
-          par = -1;
-        }
-        ctl->parent[i] = int16_t(par);
-      }
-      for (int i = tid; i < kQ * (kMaxNodes / 32); i += kThreads) (&ctl->anc[0][0])[i] = 0;
-      __syncthreads();
-      if (tid < s.m) {
-        int d = 0;
-        for (int j = ctl->parent[tid]; j >= 0; j = ctl->parent[j]) ++d;
-        ctl->depth[tid] = int16_t(d);
-        atomicMax(&ctl->dmax, d);
-        const int gj = tid - s.node0;
-        if (gj >= 0 && gj < s.n_nodes) {
-          for (int j = ctl->parent[tid]; j >= 0; j = ctl->parent[j]) ctl->anc[gj][j >> 5] |= 1u << (j & 31);
-          const int pos = s.t + d, n = entries(pos, p.window, p.stride);
-          ctl->node_p[gj] = pos;
-          ctl->node_n[gj] = n;
-          atomicMin(&ctl->seg.n_min, n);
-          atomicMax(&ctl->seg.p_max, pos);
-          // its columns: query rows tid * heads .. + heads of the sequence, within the group
-          const int lo = p.idx ? 0 : max(0, tid * p.heads - kQ * s.g);
-          const int hi = p.idx ? s.rows : min(s.rows, (tid + 1) * p.heads - kQ * s.g);
-          ctl->colmask[gj] = (hi >= 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
-        }
-      }
-      if (tid < kQ) ctl->m[tid] = -INFINITY;
-      __syncthreads();
-      if (tid == 0) {
-        Seg& q = ctl->seg;
-        q.n = p.idx ? min(p.k, q.n_min) : entries(q.t + ctl->dmax, p.window, p.stride);
-        q.full = p.idx ? 0 : q.n / kRows;
-        q.rem = q.n - kRows * q.full;
-      }
-      __syncthreads();
-    }
-    const Seg s = ctl->seg;
+    s.n_min = ctl->n_min;
+    s.n = p.idx ? min(p.k, s.n_min) : entries(s.t + ctl->dmax, p.window, p.stride);
+    s.full = p.idx ? 0 : s.n / kRows;
+    s.rem = s.n - kRows * s.full;
     // (the deepest node may be less deep than the schedule allowed for: fewer tiles)
     const int exact = s.full + (s.rem + s.w + s.m + kRows - 1) / kRows;
     const int nt = max(0, min(s.t1, exact) - s.t0);
 
     if (C::kQuant) {  // queries to f16, in place
-      const bool ok = wait_bar(&ctl->q_full, segs & 1, abort);
-      if (ok)
+      if (wait_bar(&ctl->q_full, segs & 1, abort))
+#pragma unroll 1
         for (int i = tid; i < kQBytes / 16; i += kThreads) {
           uint4 v = reinterpret_cast<uint4*>(sQ)[i];
           uint32_t* w = reinterpret_cast<uint32_t*>(&v);
@@ -627,12 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- TMA: whole tiles of bf16 rows
       if (lane == 0) {
         int issued = 0;
+#pragma unroll 1
         for (int i = 0; i < nt; ++i) {
           const int T = s.t0 + i, c = cnt + i;
           int32_t row[2];
           const bool tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, row);
           bool ok = true;
-          for (int sp = 0; sp < kParts && ok; ++sp) {
+#pragma unroll 1
+          for (int sp = 0; sp < kParts; ++sp) {
             if (c > 0) ok = wait_bar(&ctl->empty[sp], (c - 1) & 1, abort);
             if (!ok) break;
             if (tma) {
@@ -666,8 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t rd = smem_desc_sw128(smem_u32(sR), 16, 1024);
         const uint64_t ad = smem_desc_sw128(smem_u32(sR), kSlabBytes, 1024);
         const uint64_t pd = smem_desc_sw128(smem_u32(sP), 16, 1024);
+#pragma unroll 1
         for (int i = 0; i < nt && ok; ++i) {
           const int c = cnt + i;
+#pragma unroll 1
           for (int sp = 0; sp < kParts; ++sp) {
             ok = wait_bar(&ctl->full[sp], c & 1, abort);
             if (!ok) break;
@@ -695,121 +707,108 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(&ctl->o_done);  // completes once every product issued so far has
       }
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp >= kSoft0) {
       // ---------------------------------------------------------- softmax, epilogue
-      const int wq = warp & 3, half = (warp - 4) >> 2, c32 = 32 * half;
+      const int wq = warp & 3, c0 = kCols * ((warp - kSoft0) >> 2);  // row quarter (TMEM lanes), first column
       const uint32_t lane_base = uint32_t(32 * wq) << 16;
-      const int r = 32 * wq + lane;  // this thread's row
-      const uint32_t valid_cols = s.rows - c32 >= 32 ? kFull : s.rows > c32 ? (1u << (s.rows - c32)) - 1u : 0u;
-      float l[32];
+      const int r = 32 * wq + lane;   // this thread's row
+      const int q = tid - 32 * kSoft0;  // (q < 64) the query that this thread keeps the statistics of
+      const uint32_t valid_cols = s.rows - c0 >= kCols ? 0xffffu : s.rows > c0 ? (1u << (s.rows - c0)) - 1u : 0u;
+      if (q < kQ) ctl->col_pos[q] = ctl->node_p[p.idx ? 0 : (kQ * s.g + min(q, s.rows - 1)) / p.heads - s.node0];
+      float l[kCols];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) l[j] = 0.f;
+      for (int j = 0; j < kCols; ++j) l[j] = 0.f;
       bool dead = false;
+#pragma unroll 1
       for (int i = 0; i < nt; ++i) {
         const int T = s.t0 + i, c = cnt + i;
         // what the row is and who sees it (while the products run)
         uint32_t seen = valid_cols;
-        bool all = !p.idx && T < s.full && kRows * (T + 1) <= s.n_min;
-        if (!all) {
+        if (p.idx || T >= s.full || kRows * (T + 1) > s.n_min) {
           int x;
           const int kind = row_kind(p, s, T, r, &x);
           if (kind == kNone) {
             seen = 0;
           } else if (kind != kComp || !p.idx) {
-            const int wpos = s.t - 1 - (kind == kWin ? (s.t - 1 - x) % p.window : 0);
+            const int wpos = kind == kWin ? s.t - 1 - (s.t - 1 - x) % p.window : 0;
             seen = 0;
+#pragma unroll 1
             for (int j = 0; j < s.n_nodes; ++j) {
               const bool v = kind == kComp ? x < ctl->node_n[j]
                              : kind == kWin ? wpos >= ctl->node_p[j] - p.window
                                             : (ctl->anc[j][x >> 5] >> (x & 31)) & 1u;
-              if (v) seen |= uint32_t(ctl->colmask[j] >> c32);
+              if (v) seen |= uint32_t(ctl->colmask[j] >> c0) & 0xffffu;
             }
           }
         }
         if (!dead) dead = !warp_wait(&ctl->s_full, c & 1, abort, lane);
         // (complete, the product has read the tile: orders the loaders' row words and scales before this)
         if (!dead) dead = !warp_wait(&ctl->full[0], c & 1, abort, lane);
-        float sc[32];
-        bool raise = false;
-        float rs = 1.f, ls = 0.f, rinv = 1.f;
+        float f = p.score_scale, ls = 0.f, rinv = 1.f;
         if (!dead) {
+          tc_fence_after();
           if (!((ctl->ok[c & 1][wq] >> lane) & 1u)) seen = 0;  // no such row, or a bad page
           if (C::kRowScale) {
-            rs = ctl->scale[c & 1][r];
+            const float rs = ctl->scale[c & 1][r];
+            f *= rs;
             ls = rs > 0.f ? __log2f(rs) : 0.f;
             rinv = rs > 0.f ? __frcp_rn(rs) : 0.f;
           }
-          tc_fence_after();
-          uint32_t raw[32];
-          tmem_ld32(tmem + lane_base + kColS + c32, raw);
-          tmem_wait_ld();
-          const float f = p.score_scale * rs;
-          if (seen != valid_cols) {
-            // a row hidden from some query: not finite there?  (a query that is not finite itself says nothing)
-            bool odd = false;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const bool hid = (valid_cols & ~seen) >> j & 1u;
-              odd |= hid && (raw[j] & 0x7f800000u) == 0x7f800000u;
-            }
-            if (odd) {
-              bool bad = false;
-              for (int sp = 0; sp < kParts; ++sp) wait_bar(&ctl->full[sp], c & 1, abort);  // (complete)
-              for (int ch = 0; ch < kDim; ch += 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(cell(sR, r, ch));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                const uint32_t e = C::kQuant ? 0x7c00u : 0x7f80u;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) bad |= (w[k] & e) == e || ((w[k] >> 16) & e) == e;
-              }
-              if (bad)
-                for (int ch = 0; ch < kDim; ch += 8)
-                  *reinterpret_cast<uint4*>(cell(sR, r, ch)) = make_uint4(0, 0, 0, 0);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            sc[j] = (seen >> j) & 1u ? fmaf(__uint_as_float(raw[j]), f, ls) : -INFINITY;
-            raise |= sc[j] > ctl->m[c32 + j] + kRaise;
-          }
         }
-        if (soft_or(raise)) {
+        // x_j - m_j; a score that passes its maximum by more than 2^8 has the maxima raised, then once more
+        float d[kCols];
+#pragma unroll 1
+        for (int again = 0; again < 2; ++again) {
+          bool raise = false;
+          if (!dead) {
+            uint32_t raw[kCols];
+            tmem_ld16(tmem + lane_base + kColS + c0, raw);
+            tmem_wait_ld();
+            if (seen != valid_cols && again == 0) hide_bad_row<C::kQuant>(raw, valid_cols & ~seen, sR, r, ctl, c);
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+              const float x = (seen >> j) & 1u ? fmaf(__uint_as_float(raw[j]), f, ls) : -INFINITY;
+              d[j] = x - ctl->m[c0 + j];
+              top = fmaxf(top, d[j]);
+            }
+            raise = top > kRaise;
+          }
+          if (again || !soft_or(raise)) break;
           // column maxima over the tile's rows; raise the maxima that were passed
           if (!dead) {
+            uint32_t raw[kCols];
+            float x[kCols];  // the scores themselves: the differences to kNoMax have lost them
+            tmem_ld16(tmem + lane_base + kColS + c0, raw);
+            tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float v = sc[j];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-              if (lane == j) ctl->wmax[wq][c32 + j] = v;
-            }
+            for (int j = 0; j < kCols; ++j)
+              x[j] = (seen >> j) & 1u ? fmaf(__uint_as_float(raw[j]), f, ls) : -INFINITY;
+            const float v = reduce_cols(x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (!(lane & 1)) ctl->part[wq][c0 + col_of(lane)] = v;
           }
           soft_sync();
-          const int q = tid - 128;
           if (q < kQ) {
-            const float mx = fmaxf(fmaxf(ctl->wmax[0][q], ctl->wmax[1][q]), fmaxf(ctl->wmax[2][q], ctl->wmax[3][q]));
+            const float mx = fmaxf(fmaxf(ctl->part[0][q], ctl->part[1][q]), fmaxf(ctl->part[2][q], ctl->part[3][q]));
             const float m = ctl->m[q];
-            float a = 1.f;
-            if (mx > m + kRaise) {
-              a = m == -INFINITY ? 0.f : exp2_approx(m - mx);
-              ctl->m[q] = mx;
-            }
-            ctl->alpha[q] = a;
+            const bool up = mx > m + kRaise;
+            ctl->alpha[q] = up ? exp2_approx(m - mx) : 1.f;
+            if (up) ctl->m[q] = mx;
           }
           soft_sync();
           if (!dead) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) l[j] *= ctl->alpha[c32 + j];
+            for (int j = 0; j < kCols; ++j) l[j] *= ctl->alpha[c0 + j];
             if (i > 0) {  // the accumulator too (this tile's scores are in, so the products before them are)
 #pragma unroll 1
               for (int ct = 0; ct < kParts; ++ct) {
-                uint32_t o[32];
-                const uint32_t addr = tmem + lane_base + kColO + kQ * ct + c32;
-                tmem_ld32(addr, o);
+                uint32_t o[kCols];
+                const uint32_t addr = tmem + lane_base + kColO + kQ * ct + c0;
+                tmem_ld16(addr, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * ctl->alpha[c32 + j]);
-                tmem_st32(addr, o);
+                for (int j = 0; j < kCols; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * ctl->alpha[c0 + j]);
+                tmem_st16(addr, o);
               }
               tmem_wait_st();
             }
@@ -818,31 +817,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (dead) continue;
         uint8_t* prow = sP + r * 128;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kCols / 8; ++u) {
           uint32_t pk[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 8 * u + 2 * e;
-            const float ma = ctl->m[c32 + j], mb = ctl->m[c32 + j + 1];
-            const float a = exp2_approx(sc[j] - (ma == -INFINITY ? 0.f : ma));
-            const float b = exp2_approx(sc[j + 1] - (mb == -INFINITY ? 0.f : mb));
-            // the weights the product uses are the ones l sums
-            float ra, rb;
-            if (C::kQuant) {
-              pk[e] = f32x2_to_f16x2_sat(a, b);
-              asm("{\n\t.reg .f16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
-                  : "=f"(ra), "=f"(rb)
-                  : "r"(pk[e]));
+            const float a = exp2_approx(d[j]), b = exp2_approx(d[j + 1]);
+            // the weights the product uses are the ones l sums (row scales: the stored row's weight carries its
+            // scale, the denominator's does not)
+            pk[e] = C::kQuant ? f32x2_to_f16x2_sat(a, b) : cvt_bf16x2(a, b);
+            if (C::kRowScale) {
+              l[j] = fmaf(a, rinv, l[j]);
+              l[j + 1] = fmaf(b, rinv, l[j + 1]);
+            } else if (C::kQuant) {
+              const float2 w = f16x2_to_f32(pk[e]);
+              l[j] += w.x;
+              l[j + 1] += w.y;
             } else {
-              pk[e] = cvt_bf16x2(a, b);
-              ra = bf16lo(pk[e]);
-              rb = bf16hi(pk[e]);
+              l[j] += bf16lo(pk[e]);
+              l[j + 1] += bf16hi(pk[e]);
             }
-            // (row scales: the stored row's weight carries its scale, the denominator's does not)
-            l[j] = C::kRowScale ? fmaf(a, rinv, l[j]) : l[j] + ra;
-            l[j + 1] = C::kRowScale ? fmaf(b, rinv, l[j + 1]) : l[j + 1] + rb;
           }
-          *reinterpret_cast<uint4*>(prow + (((4 * half + u) ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(prow + (((c0 / 8 + u) ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -850,82 +846,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl->p_full);
       }
       // ---- epilogue
-      if (!dead) dead = !warp_wait(&ctl->o_done, segs & 1, abort, lane);
-      if (!dead) {
-        tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float v = l[j];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-          if (lane == j) ctl->lsum[wq][c32 + j] = v;
-        }
+      {
+        const float v = reduce_cols(l, lane, [](float a, float b) { return a + b; });
+        if (!(lane & 1)) ctl->part[wq][c0 + col_of(lane)] = v;
       }
+      if (!dead) dead = !warp_wait(&ctl->o_done, segs & 1, abort, lane);
+      tc_fence_after();
       soft_sync();
       const bool final_out = s.t0 == 0 && s.t1 == s.tiles;
       const int slot = 2 * cta + (s.t0 == 0 ? 1 : 0);
-      const int q = tid - 128;
       if (!dead && q < kQ) {
-        const float L = (ctl->lsum[0][q] + ctl->lsum[1][q]) + (ctl->lsum[2][q] + ctl->lsum[3][q]);
-        if (final_out) {
-          ctl->alpha[q] = L == 0.f ? 0.f : __frcp_rn(L);  // no row: zeros
-        } else {
-          int pos = 0;
-          for (int j = 0; j < s.n_nodes; ++j)
-            if ((ctl->colmask[j] >> q) & 1u) pos = ctl->node_p[j];
+        const float L = (ctl->part[0][q] + ctl->part[1][q]) + (ctl->part[2][q] + ctl->part[3][q]);
+        ctl->alpha[q] = !final_out ? 1.f : L == 0.f ? 0.f : __frcp_rn(L);  // (no row: zeros)
+        if (!final_out) {
           // (a query that is not finite: its NaN has to pass the merge, which skips runs without rows)
-          p.ml[size_t(slot) * kQ + q] = make_float4(L != L ? INFINITY : ctl->m[q], L, __int_as_float(pos), 0.f);
+          p.ml[size_t(slot) * kQ + q] = make_float4(L != L ? INFINITY : ctl->m[q], L, __int_as_float(ctl->col_pos[q]), 0.f);
           if (q == 0) p.rec[slot] = Rec{1, s.b, s.g, s.t0, s.t1, s.tiles, s.row0, s.rows};
         }
       }
       soft_sync();
       if (!dead && nt > 0) {
-        const int r0 = kDim - p.rope_dim;
+        const int r0 = kDim - p.rope_dim, odd = lane & 1;
 #pragma unroll 1
         for (int ct = 0; ct < kParts; ++ct) {
-          const int ch = 128 * ct + 32 * wq + lane;
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_base + kColO + kQ * ct + c32, o);
+          // lane pairs swap, so that each lane has both channels ch, ch + 1 of every other column
+          const int ch = 128 * ct + 32 * wq + lane - odd;
+          uint32_t o[kCols];
+          tmem_ld16(tmem + lane_base + kColO + kQ * ct + c0, o);
           tmem_wait_ld();
-          if (!final_out) {
-            float* dst = p.o_part + (size_t(slot) * kQ + c32) * kDim + ch;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) dst[size_t(j) * kDim] = __uint_as_float(o[j]);
-            continue;
-          }
-          const bool rot = ch >= r0;
           float cs = 1.f, sn = 0.f;
-          int node = -1;
-          const size_t base = size_t(s.row0 + c32) * kDim + ch;
+          int pos = -1;
+          const bool rot = final_out && ch >= r0;
+          const double theta = rot ? p.rope.theta_pi[(ch - r0) >> 1] : 0.0;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float a = ctl->alpha[c32 + j];
-            float v = a != 0.f ? __uint_as_float(o[j]) * a : 0.f;
-            if (128 * ct + 128 > r0) {
-              const int nj = p.idx ? 0 : (kQ * s.g + min(c32 + j, s.rows - 1)) / p.heads - s.node0;
-              if (nj != node) {
-                node = nj;
-                if (rot) rope_rotation(p.rope.theta_pi[(ch - r0) >> 1], -double(ctl->node_p[nj]), &cs, &sn);
+          for (int jj = 0; jj < kCols / 2; ++jj) {
+            const float va = __uint_as_float(o[2 * jj]), vb = __uint_as_float(o[2 * jj + 1]);
+            const float got = __shfl_xor_sync(kFull, odd ? va : vb, 1);
+            const int col = c0 + 2 * jj + odd;
+            const float a = ctl->alpha[col];
+            float x = odd ? got : va, y = odd ? vb : got;
+            x = a == 0.f ? 0.f : x * a;
+            y = a == 0.f ? 0.f : y * a;
+            if (rot) {
+              const int pc = ctl->col_pos[col];
+              if (pc != pos) {
+                pos = pc;
+                rotation(theta, pos, &cs, &sn);
               }
-              const float other = __shfl_xor_sync(kFull, v, 1);  // channel ch ^ 1 of the same query
-              if (rot) v = (ch & 1) ? fmaf(other, sn, v * cs) : fmaf(v, cs, -other * sn);
+              const float t = x;
+              x = fmaf(t, cs, -y * sn);
+              y = fmaf(t, sn, y * cs);
             }
-            if (c32 + j < s.rows) {
-              if (p.out_fp32) static_cast<float*>(p.out)[base + size_t(j) * kDim] = v;
-              else static_cast<uint16_t*>(p.out)[base + size_t(j) * kDim] = uint16_t(cvt_bf16x2(v, 0.f));
+            if (!final_out) {
+              *reinterpret_cast<float2*>(p.o_part + (size_t(slot) * kQ + col) * kDim + ch) = make_float2(x, y);
+            } else if (col < s.rows) {
+              const size_t at = size_t(s.row0 + col) * kDim + ch;
+              if (p.out_fp32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
+              else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = cvt_bf16x2(x, y);
             }
           }
         }
-        tc_fence_before();
       }
-    } else if (warp >= 12) {
+    } else {
       // ---------------------------------------------------------- loaders
-      const int lw = warp - 12, r = 32 * lw + lane;
+      const int lw = warp - kLoad0, r = 32 * lw + lane;
       bool ok = true;
+#pragma unroll 1
       for (int i = 0; i < nt && ok; ++i) {
         const int T = s.t0 + i, c = cnt + i;
         int32_t rows2[2];
         if (!C::kQuant && T < s.full && tma_rows(p, s.b, T, rows2)) {
+#pragma unroll 1
           for (int sp = 0; sp < kParts && ok; ++sp) {
             if (c > 0) ok = warp_wait(&ctl->empty[sp], (c - 1) & 1, abort, lane);
             if (ok && lane == 0) {
@@ -939,11 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Rows* src = row_source(p, s, T, r, &row);
         const uint8_t* my = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
         const uint32_t have = __ballot_sync(kFull, src != nullptr);
-        float my_scale = 0.f;
-        const uint8_t* mysc = nullptr;
-        if (C::kRowScale && src) my_scale = static_cast<const float*>(src->scales)[row];
-        if (FMT == DSV4KV_FP4_E2M1_G16 && src) mysc = static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16);
         if constexpr (!C::kQuant) {
+#pragma unroll 1
           for (int sp = 0; sp < kParts && ok; ++sp) {
             if (c > 0) ok = warp_wait(&ctl->empty[sp], (c - 1) & 1, abort, lane);
             if (!ok) break;
@@ -974,22 +962,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async_wait_group<0>();
           hand(3);
         } else {
+          float my_scale = 0.f;
+          const uint8_t* mysc = nullptr;
+          if (C::kRowScale && src) my_scale = static_cast<const float*>(src->scales)[row];
+          if (FMT == DSV4KV_FP4_E2M1_G16 && src)
+            mysc = static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16);
           const float my_inv = my_scale > 0.f ? __frcp_rn(my_scale) : 0.f;
-          QuantPart<FMT> part[2];
+          using Part = QuantPart<FMT>;
+          Part part[2];
           part[0].fetch(my, mysc, 0, lane);
 #pragma unroll
-          for (int sp = 0; sp < kParts; ++sp) {
-            if (sp + 1 < kParts) part[(sp + 1) & 1].fetch(my, mysc, sp + 1, lane);
-            if (ok && c > 0) ok = warp_wait(&ctl->empty[sp], (c - 1) & 1, abort, lane);
+          for (int k = 0; k < Part::kCount; ++k) {
+            const int sp = min(k, kParts - 1);
+            if (k + 1 < Part::kCount) part[(k + 1) & 1].fetch(my, mysc, k + 1, lane);
+            if (ok && c > 0 && k < kParts) ok = warp_wait(&ctl->empty[sp], (c - 1) & 1, abort, lane);
             if (ok) {
-              if (sp == 0) {
+              if (k == 0) {
                 if (lane == 0) ctl->ok[c & 1][lw] = have;
                 if (C::kRowScale) ctl->scale[c & 1][r] = my_scale;
               }
-              part[sp & 1].put(sR, lw, sp, my_inv, lane);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl->full[sp]);
+              part[k & 1].put(sR, lw, k, my_inv, lane);
+              if (k < kParts - 1 || k == Part::kCount - 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->full[sp]);
+              }
             }
           }
         }
@@ -997,30 +994,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cnt += nt;
     ++segs;
+    if (whole) {
+      g_next += P;
+    } else {
+      left -= s.t1 - s.t0;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (ctl->abort) break;
+    // ---- the next part
     if (whole) {
-      g_next += P;
       for (int b = tid; b < p.batch; b += kThreads)
         if (ctl->gpre[b] <= g_next && g_next < ctl->gpre[b + 1]) {
-          ctl->seg.b = b;
-          ctl->seg.g = g_next - ctl->gpre[b];
-          ctl->seg.t0 = 0;
+          ctl->b = b;
+          ctl->g = g_next - ctl->gpre[b];
+          ctl->t0 = 0;
         }
-    } else {
-      left -= s.t1 - s.t0;
-      if (tid == 0 && left > 0) {
-        Seg& q = ctl->seg;
-        q.t0 = 0;
-        q.g = s.g + 1;
-        while (q.b < p.batch && q.g >= ctl->gpre[q.b + 1] - ctl->gpre[q.b]) {
-          ++q.b;
-          q.g = 0;
-        }
+    } else if (tid == 0 && left > 0) {
+      int b = s.b, g = s.g + 1;
+      while (b < p.batch && g >= ctl->gpre[b + 1] - ctl->gpre[b]) {
+        ++b;
+        g = 0;
       }
+      ctl->b = b;
+      ctl->g = g;
+      ctl->t0 = 0;
     }
+    __syncthreads();
   }
   __syncthreads();
   if (tid == 0 && ctl->abort) set_status(p.status, DSV4KV_DEV_TIMEOUT);
@@ -1037,7 +1038,7 @@ __global__ void __launch_bounds__(256) tree_combine(const __grid_constant__ Para
   const Rec own = p.rec[2 * c + 1];
   if (!own.valid || j >= own.rows) return;
   // the runs behind it: first slots of the next CTAs, until one ends the group
-  float M = -INFINITY;
+  float M = kNoMax;
   int last = c;
   {
     int end = own.t1;
@@ -1060,8 +1061,8 @@ __global__ void __launch_bounds__(256) tree_combine(const __grid_constant__ Para
   for (int x = c; x <= last; ++x) {
     const size_t slot = x == c ? 2 * c + 1 : 2 * x;
     const float4 ml = p.ml[slot * kQ + j];
-    const float w = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
-    if (w == 0.f) continue;
+    if (ml.y == 0.f) continue;  // it saw no row (its O may be unwritten)
+    const float w = exp2_approx(ml.x - M);
     L = fmaf(w, ml.y, L);
     const float4* src = reinterpret_cast<const float4*>(p.o_part + (slot * kQ + j) * kDim) + lane;
 #pragma unroll
@@ -1073,13 +1074,12 @@ __global__ void __launch_bounds__(256) tree_combine(const __grid_constant__ Para
       o[q].w = fmaf(w, v.w, o[q].w);
     }
   }
-  const float inv = M == -INFINITY ? 0.f : __frcp_rn(L);
+  const float inv = L == 0.f ? 0.f : __frcp_rn(L);
   const int r0 = kDim - p.rope_dim;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int ch = 128 * q + 4 * lane;
     float v[4] = {o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv};
-    if (M == -INFINITY) v[0] = v[1] = v[2] = v[3] = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; e += 2)
       if (ch + e >= r0) {
