@@ -612,7 +612,8 @@ static bool tree_sizes_ok(int32_t batch, int32_t heads, int32_t max_nodes, int64
                           int32_t stride, int32_t k) {
   return batch >= 1 && batch <= 1024 && heads >= 1 && heads <= 128 && max_nodes >= 1 && max_nodes <= 256 && nodes >= 0 &&
          nodes < ((int64_t(1) << 31) - 1024) / heads && t_max >= 0 && t_max < kMaxLen && window >= 0 &&
-         window <= kMaxWindow && stride >= 1 && k >= 0 && k <= 2048;
+         window <= kMaxWindow && stride >= 1 && k >= 0 && k <= 2048 &&
+         tree_units_ok(batch, heads, max_nodes, nodes, t_max, window, stride, k);
 }
 
 DSV4KV_API size_t dsv4kv_tree_decode_paged_workspace_bytes(int32_t batch, int32_t heads, int32_t dim,
@@ -638,7 +639,8 @@ DSV4KV_API dsv4kv_status dsv4kv_tree_decode_paged(const void* q, const dsv4kv_pa
   if (idx && (k < 1 || k > 2048)) return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: k must be in [1, 2048]", what);
   if (!tree_sizes_ok(batch, heads, max_nodes, nodes, t_max, window, stride, idx ? k : 0))
     return set_error(DSV4KV_ERR_UNSUPPORTED,
-                     "%s: batch must be <= 1024, heads <= 128, max_nodes <= 256, t_max < 2^30, window <= 65536", what);
+                     "%s: batch must be <= 1024, heads <= 128, max_nodes <= 256, t_max < 2^30, window <= 65536, and the "
+                     "128-row tiles of all groups of 128 query rows fewer than 2^31", what);
   if (rope_dim < 0 || rope_dim > 512 || (rope_dim & 1))
     return set_error(DSV4KV_ERR_INVALID_ARG, "%s: bad rope_dim", what);
   if (!(rope_base > 0.0)) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: rope_base must be > 0", what);

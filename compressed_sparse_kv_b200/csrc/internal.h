@@ -149,6 +149,7 @@ struct TreeArgs {
   int out_fp32;
   void* out;
 };
+bool tree_units_ok(int batch, int heads, int max_nodes, int64_t nodes, int64_t t_max, int window, int stride, int k);
 size_t tree_ws_bytes(int batch, int heads, int max_nodes, int64_t nodes, int64_t t_max, int window, int stride, int k);
 dsv4kv_status tree_decode_launch(const TreeArgs& a, void* ws, cudaStream_t stream);
 
