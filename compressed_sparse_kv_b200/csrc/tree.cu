@@ -64,8 +64,9 @@ constexpr int kQSlab = kQ * 128;        // 64 channels of the queries
 constexpr int kQBytes = 8 * kQSlab;     // 64 KB
 constexpr int kKSlab = kKeys * 128;     // 64 channels of the keys
 constexpr int kKBytes = 8 * kKSlab;     // 64 KB
-constexpr int kVSlab = kRows * 128;     // 64 channels of the values
-constexpr int kVBytes = 4 * kVSlab;     // 64 KB
+constexpr int kVSlab = 64 * 128;        // 64 channels of 64 of the values
+constexpr int kVPart = 4 * kVSlab;      // 64 values, 32 KB
+constexpr int kVBytes = 2 * kVPart;     // 64 KB
 constexpr int kPBytes = 2 * kQ * 128;   // weights: 2 chunks of 64 rows
 constexpr int kMaxBatch = 1024;
 constexpr int kMaxNodes = 256;
@@ -309,7 +310,9 @@ __device__ __forceinline__ const Rows* row_source(const Params& p, const Seg& s,
 // ---------------------------------------------------------------- loader warps
 __device__ __forceinline__ uint32_t swz(int r, int ch) { return r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4); }
 __device__ __forceinline__ uint8_t* key_cell(uint8_t* sK, int r, int ch) { return sK + (ch >> 6) * kKSlab + swz(r, ch); }
-__device__ __forceinline__ uint8_t* val_cell(uint8_t* sV, int r, int ch) { return sV + (ch >> 6) * kVSlab + swz(r, ch); }
+__device__ __forceinline__ uint8_t* val_cell(uint8_t* sV, int r, int ch) {
+  return sV + (r >> 6) * kVPart + (ch >> 6) * kVSlab + swz(r & 63, ch);
+}
 
 __device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* p, int src) {
   return reinterpret_cast<const uint8_t*>(__shfl_sync(kFull, reinterpret_cast<uint64_t>(p), src));
@@ -418,8 +421,8 @@ __device__ __noinline__ void zero_bad_row(uint8_t* sV, int r) {
 // ---------------------------------------------------------------- the kernel
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_comp,
-                const __grid_constant__ Params p) {
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_key,
+                const __grid_constant__ CUtensorMap tm_val, const __grid_constant__ Params p) {
   using C = Cfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -457,7 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
   if (tid == 64) {
     prefetch_tmap(&tm_q);
-    if (!C::kQuant) prefetch_tmap(&tm_comp);
+    if (!C::kQuant) {
+      prefetch_tmap(&tm_key);
+      prefetch_tmap(&tm_val);
+    }
   }
   tc_fence_before();
   pdl_wait();
@@ -565,8 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bar = C::kQuant ? smem_u32(&ctl->q_full) : lead_addr(&ctl->q_ready);
       if (C::kQuant) mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
       else if (rank == 0) mbar_arrive_expect_tx(&ctl->q_ready, 2 * kQBytes);
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) tma_load_2d_pair(sQ + c * kQSlab, &tm_q, bar, 64 * c, s.row0);
+      tma_load_3d_pair(sQ, &tm_q, bar, 0, s.row0, 0);
     }
     if (tid == kThreads - 1) {
       ctl->n_min = kNever;
@@ -617,19 +622,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 1) {
       // ---------------------------------------------------------- products (the first CTA issues them)
-      if (lane == 0 && rank == 0) {
+      if (rank == 0) {
+        const uint32_t me = elect_lane();
         uint64_t idle = 0;
         auto stuck = [&]() {  // nothing was ready: bounded
           const uint64_t now = globaltimer();
           if (idle == 0) idle = now;
-          if (*abort || now - idle > kWaitLimitNs) {
-            *abort = 1;
-            return true;
-          }
-          return false;
+          if (now - idle > kWaitLimitNs) *abort = 1;
+          return __any_sync(kFull, *abort != 0) != 0;
+        };
+        auto ready = [&](uint64_t* bar, uint32_t parity) {
+          return __all_sync(kFull, mbar_test_wait_cluster(bar, parity)) != 0;
         };
         bool ok = true;
-        while (ok && !mbar_test_wait_cluster(&ctl->q_ready, segs & 1)) ok = !stuck();
+        while (ok && !ready(&ctl->q_ready, segs & 1)) ok = !stuck();
         const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t pd = smem_desc_sw128(smem_u32(sP), 16, 1024);
@@ -638,36 +644,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         idle = 0;
 #pragma unroll 1
         while (ok && pv < nt) {
-          if (pv < qk && mbar_test_wait_cluster(&ctl->p_full, (cnt + pv) & 1) &&
-              mbar_test_wait_cluster(&ctl->v_full, (cnt + pv) & 1)) {
+          if (pv < qk && ready(&ctl->p_full, (cnt + pv) & 1) && ready(&ctl->v_full, (cnt + pv) & 1)) {
             tc_fence_after();
-#pragma unroll 1
+#pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int kr = 0; kr < kRows / 16; ++kr)
-                mma_f16_pair(tmem + kColO + 128 * n, pd + (((kr >> 2) * kQSlab + (kr & 3) * 32) >> 4),
-                             vd + ((2 * n * kVSlab + kr * 2048) >> 4), C::kIdescPV, (pv > 0 || kr > 0) ? 1u : 0u);
-            mma_commit_pair(&ctl->v_empty);
+                mma_f16_pair(me, tmem + kColO + 128 * n, pd + (((kr >> 2) * kQSlab + (kr & 3) * 32) >> 4),
+                             vd + (((kr >> 2) * kVPart + (kr & 3) * 2048 + 2 * n * kVSlab) >> 4), C::kIdescPV,
+                             (pv > 0 || kr > 0) ? 1u : 0u);
+            mma_commit_pair(me, &ctl->v_empty);
             ++pv;
             idle = 0;
-          } else if (qk < nt && qk < pv + 2 && mbar_test_wait_cluster(&ctl->k_full, (cnt + qk) & 1)) {
+          } else if (qk < nt && qk < pv + 2 && ready(&ctl->k_full, (cnt + qk) & 1)) {
             tc_fence_after();
             const int sb = (cnt + qk) & 1;
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < 8; ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_f16_pair(tmem + kColS + 64 * sb, qd + ((c * kQSlab + kk * 32) >> 4), kd + ((c * kKSlab + kk * 32) >> 4),
-                             C::kIdescQK, (c | kk) ? 1u : 0u);
-            mma_commit_pair(&ctl->s_full[sb]);
-            mma_commit_pair(&ctl->k_empty);
+                mma_f16_pair(me, tmem + kColS + 64 * sb, qd + ((c * kQSlab + kk * 32) >> 4),
+                             kd + ((c * kKSlab + kk * 32) >> 4), C::kIdescQK, (c | kk) ? 1u : 0u);
+            mma_commit_pair(me, &ctl->s_full[sb]);
+            mma_commit_pair(me, &ctl->k_empty);
             ++qk;
             idle = 0;
           } else {
             ok = !stuck();
           }
         }
-        mma_commit_pair(&ctl->o_done);  // completes once every product issued so far has
+        mma_commit_pair(me, &ctl->o_done);  // completes once every product issued so far has
         if (!ok) wait_drain(&ctl->o_done, segs & 1);
       }
     } else if (warp >= kSoft0) {
@@ -937,11 +943,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bar = lead_addr(&ctl->v_full);
             if (vw == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->v_full, 2 * kVBytes);
             else mbar_arrive_cluster(bar);
-            if (vw == 0)
-#pragma unroll 1
-              for (int x = 0; x < 8; ++x)
-                tma_load_2d_pair(sV + (x >> 1) * kVSlab + (x & 1) * (kVSlab / 2), &tm_comp, bar,
-                                 kHalf * rank + 64 * (x >> 1), trow[x & 1]);
+            if (vw == 0) {
+              tma_load_3d_pair(sV, &tm_val, bar, 0, trow[0], 4 * rank);
+              tma_load_3d_pair(sV + kVPart, &tm_val, bar, 0, trow[1], 4 * rank);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->v_here);  // (nobody waits for a whole tile's)
@@ -1005,9 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             if (kw == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->k_full, 2 * kKBytes);
             else mbar_arrive_cluster(bar);
-            if (kw == 0)
-#pragma unroll 1
-              for (int x = 0; x < 8; ++x) tma_load_2d_pair(sK + x * kKSlab, &tm_comp, bar, 64 * x, rank ? trow[1] : trow[0]);
+            if (kw == 0) tma_load_3d_pair(sK, &tm_key, bar, 0, rank ? trow[1] : trow[0], 0);
           }
           __syncwarp();
           continue;
@@ -1162,7 +1165,8 @@ Layout layout(int P) {
 }
 
 template <int FMT>
-cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tc, const Params& p, int P, cudaStream_t stream) {
+cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int P,
+                        cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
   if (!done_on_device(ready)) {
     const cudaError_t e =
@@ -1170,7 +1174,7 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tc, const Para
     if (e != cudaSuccess) return e;
     mark_done_on_device(ready);
   }
-  return launch_pdl_cluster(tree_kernel<FMT>, dim3(unsigned(2 * P)), dim3(kThreads), kSmemBytes, 2, stream, tq, tc, p);
+  return launch_pdl_cluster(tree_kernel<FMT>, dim3(unsigned(2 * P)), dim3(kThreads), kSmemBytes, 2, stream, tq, tk, tv, p);
 }
 
 Rows rows_of(const dsv4kv_cache& c, const PageDesc& pg) {
@@ -1216,20 +1220,23 @@ dsv4kv_status tree_decode_launch(const TreeArgs& a, void* ws, cudaStream_t strea
   p.ml = reinterpret_cast<float4*>(base + lay.ml);
   p.o_part = reinterpret_cast<float*>(base + lay.o);
   rope_table_fill(&p.rope, a.rope_dim, a.rope_base);
-  CUtensorMap tq{}, tc{};
-  if (!encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDim, uint64_t(a.nodes) * a.heads, kDim * 2, 64, kQ,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+  // boxes of 64 rows x 8 (queries, keys) or 4 (values) chunks of 64 channels, chunk after chunk in shared memory
+  CUtensorMap tq{}, tk{}, tv{};
+  if (!encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 64, uint64_t(a.nodes) * a.heads, 8, kDim * 2, 128, 64, kQ,
+                      8, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(DSV4KV_ERR_CUDA, "tree_decode_paged: tensor map of q");
   if (a.comp.fmt == DSV4KV_BF16 && a.comp.codes &&
-      !encode_tmap_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, kDim, uint64_t(a.comp.rows), kDim * 2, 64, 64,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+      (!encode_tmap_3d(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, 64, uint64_t(a.comp.rows), 8, kDim * 2, 128, 64,
+                       kKeys, 8, CU_TENSOR_MAP_SWIZZLE_128B) ||
+       !encode_tmap_3d(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, 64, uint64_t(a.comp.rows), 8, kDim * 2, 128, 64,
+                       64, 4, CU_TENSOR_MAP_SWIZZLE_128B)))
     return set_error(DSV4KV_ERR_CUDA, "tree_decode_paged: tensor map of the compressed cache");
   cudaError_t e;
   switch (a.comp.fmt) {
-    case DSV4KV_BF16: e = launch_tree<DSV4KV_BF16>(tq, tc, p, P, stream); break;
-    case DSV4KV_FP8_E4M3_ROW: e = launch_tree<DSV4KV_FP8_E4M3_ROW>(tq, tc, p, P, stream); break;
-    case DSV4KV_FP4_E2M1_G16: e = launch_tree<DSV4KV_FP4_E2M1_G16>(tq, tc, p, P, stream); break;
-    default: e = launch_tree<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(tq, tc, p, P, stream); break;
+    case DSV4KV_BF16: e = launch_tree<DSV4KV_BF16>(tq, tk, tv, p, P, stream); break;
+    case DSV4KV_FP8_E4M3_ROW: e = launch_tree<DSV4KV_FP8_E4M3_ROW>(tq, tk, tv, p, P, stream); break;
+    case DSV4KV_FP4_E2M1_G16: e = launch_tree<DSV4KV_FP4_E2M1_G16>(tq, tk, tv, p, P, stream); break;
+    default: e = launch_tree<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(tq, tk, tv, p, P, stream); break;
   }
   if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "tree_kernel: %s", cudaGetErrorString(e));
   dsv4kv_status st = check_launch("tree_kernel");
