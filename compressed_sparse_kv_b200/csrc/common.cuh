@@ -80,6 +80,17 @@ __device__ __forceinline__ void set_status(uint32_t* status, uint32_t flag) {
   if (status) atomicOr(status, flag);
 }
 
+// Largest b in [0, n) with pre[b] <= x (pre ascending, pre[0] = 0).
+__device__ __forceinline__ int find_seq(const int32_t* pre, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // ----------------------------------------------------------------- thread-block clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -282,18 +293,12 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 // ----------------------------------------------------------------- CTA pairs (cta_group::2, clusters of two)
 // Address of `p` (shared memory of this CTA) in the pair's CTA of rank 0.
 __device__ __forceinline__ uint32_t lead_addr(const void* p) { return dsmem_addr(p, 0); }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, "
-      "0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// Arrive on a barrier of either CTA of the pair (cluster address).  What the arriving thread hands over lies in its own
+// CTA's shared memory and is read there by the pair's products: the writers' proxy fence has completed those writes before
+// the arrival leaves, so the arrival is not given cluster scope (a cluster-wide release drains every outstanding
+// access of the SM: 1.3 us a tile under load).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // A tile into this CTA's shared memory, completing on a barrier of either CTA of the pair (`bar`: cluster address).
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,

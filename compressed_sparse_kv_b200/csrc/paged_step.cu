@@ -76,17 +76,6 @@ __device__ __forceinline__ uint64_t block_prefix(int batch, F f, S store) {
   return carry;
 }
 
-// Largest b in [0, n) with pre[b] <= x (pre ascending, pre[0] = 0).
-__device__ __forceinline__ int find_seq(const int32_t* pre, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ int64_t clamp_len(int64_t t, int64_t t_max, uint32_t* status) {
   if (t >= 0 && t <= t_max) return t;
   set_status(status, DSV4KV_DEV_BAD_LENGTH);

@@ -70,11 +70,7 @@ constexpr int kVBytes = 2 * kVPart;     // 64 KB
 constexpr int kPBytes = 2 * kQ * 128;   // weights: 2 chunks of 64 rows
 constexpr int kMaxBatch = 1024;
 constexpr int kMaxNodes = 256;
-// warps: 0 set-up and queries, 1 products, 2-5 keys, 6-7 values, 8-23 softmax and epilogue
-constexpr int kThreads = 768;
-constexpr int kKey0 = 2, kKeyWarps = 4, kVal0 = 6, kValWarps = 2, kSoft0 = 8;
-constexpr int kSoftWarps = 16, kSoftThreads = 32 * kSoftWarps;
-constexpr int kCols = 16;  // rows of a tile per softmax thread
+constexpr int kKey0 = 2, kKeyWarps = 4, kVal0 = kKey0 + kKeyWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;    // O: 2 x 128 columns
 constexpr uint32_t kColS = 256;  // S: 2 buffers of 64 columns
@@ -82,12 +78,21 @@ constexpr float kRaise = 8.0f;   // log2 units a score may pass the running maxi
 constexpr float kNoMax = -1e30f;  // a maximum that nothing has reached yet
 constexpr int kSplitCost = 3;    // tiles that a cut group's partial sums and merge cost
 
+// Warps: 0 schedule and queries, 1 products, 2-5 keys, then the value loaders, then the softmax and epilogue.  bf16
+// rows need few loader threads (TMA, cp.async) and 16 softmax warps; quantised rows are converted by 8 loader warps,
+// and 8 softmax warps leave them the registers for 8 loads of 16 bytes in flight each.
 template <int FMT>
 struct Cfg {
   static constexpr bool kQuant = FMT != DSV4KV_BF16;
   static constexpr bool kRowScale = FMT == DSV4KV_FP8_E4M3_ROW || FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16;
   static constexpr uint32_t kIdescQK = kQuant ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
   static constexpr uint32_t kIdescPV = kQuant ? idesc_f16(128, 256, 0, 1) : idesc_bf16(128, 256, 0, 1);
+  static constexpr int kValWarps = kQuant ? 4 : 2, kValRows = kRows / kValWarps;
+  static constexpr int kSoft0 = kVal0 + kValWarps, kSoftWarps = kQuant ? 8 : 16;
+  static constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kSoft0 + kSoftWarps);
+  static constexpr int kGroups = kSoftWarps / 4;  // softmax warps that share a quarter of the TMEM lanes
+  static constexpr int kCols = 64 / kGroups;      // rows of a tile per softmax thread
+  static constexpr int kChans = 256 / kGroups;    // output channels per softmax thread
 };
 
 // A cut group's run of tiles in one pair; slot 2c: the run does not start the group, 2c + 1: it starts it.
@@ -122,9 +127,7 @@ struct Params {
 struct Seg {  // the part of a group that a pair works on
   int b, g, t0, t1, tiles;  // sequence, group within it, tiles [t0, t1) of `tiles`
   int t, w, m, c0;          // position, window rows, drafted nodes, first node
-  int row0, rows;           // this CTA's first query row and their number
-  int node0, n_nodes;       // the nodes they belong to (numbers within the sequence)
-  int n, full;              // compressed rows listed, whole tiles of them
+  int n, full;              // compressed rows listed (the most any node may see), whole tiles that every node sees
 };
 
 // Who sees a row: the positions [lo, hi]; lo < 0: drafted node -1 - lo, its descendants.
@@ -135,18 +138,18 @@ constexpr int kNever = 0x7fffffff;
 
 struct __align__(16) Ctl {
   // in the pair's first CTA: both CTAs' loads and weights arrive on these
-  uint64_t q_ready, k_full, v_full, p_full;
+  uint64_t q_ready, k_full[2], v_full[2], p_full[2];
   // in each CTA
-  uint64_t q_full, info[2], v_here;
-  uint64_t s_full[2], k_empty, v_empty, o_done;
+  uint64_t q_full, meta, info[2], v_here[2];
+  uint64_t s_full[2], k_empty[2], v_empty[2], o_done;
   uint32_t tmem_base;
   volatile int abort;
-  int n_min, n_max;  // least / greatest entry count of the group's nodes
-  int node_pos;      // (selected form) the node's position
-  int b, g, t0;  // the next part to work on
+  int p_max;      // greatest position of the group's nodes
+  int node_pos;   // (selected form) the node's position
+  int b, g, t0;   // (equal runs) where this pair's run starts
   int whole, share, units;
   Key key[2][kRows];              // the rows of a tile that the loader warps brought
-  uint32_t plain[2][kValWarps];   // all of a warp's rows are there and every query sees them
+  uint32_t plain[2][4];           // all of a value warp's rows are there and every query sees them
   __align__(16) float scale[2][kRows];
   __align__(16) float lscale[2][kRows];  // log2 of the scale
   __align__(16) float iscale[2][kRows];  // 1 / the scale
@@ -198,23 +201,30 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   if (lane == 0) ok = wait_bar(bar, parity, abort);
   return __shfl_sync(kFull, ok, 0);
 }
-__device__ __forceinline__ bool soft_or(bool pred) {  // over the softmax threads
+template <int N>
+__device__ __forceinline__ bool soft_or(bool pred) {  // over the N softmax threads
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.cta.red.or.pred po, 1, 512, pi;\n\tselp.u32 "
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.cta.red.or.pred po, 1, %2, pi;\n\tselp.u32 "
       "%0, 1, 0, po;\n\t}"
       : "=r"(r)
-      : "r"(uint32_t(pred))
+      : "r"(uint32_t(pred)), "n"(N)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {  // max relative error ~2^-22, far below the weights' 16 bits
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
 
 __device__ __noinline__ void rotation(double theta_pi, int pos, float* cs, float* sn) {
   rope_rotation(theta_pi, -double(pos), cs, sn);
@@ -273,38 +283,48 @@ __device__ __forceinline__ bool tma_rows(const Params& p, int b, int T, int32_t 
 }
 
 // Row r of tile T: its cache and pool row (null: there is none, or no query of the group sees it) and who sees it.
+// Whole tiles (T < s.full) need nothing of the tree.
 __device__ __forceinline__ const Rows* row_source(const Params& p, const Seg& s, const Ctl* ctl, int T, int r,
                                                   int64_t* row, Key* key) {
   const int u = kRows * T + r, j = u - s.n;
-  *row = -1;
+  const Rows* src = nullptr;
+  int i = -1;
   *key = Key{0, kNever};
   if (j < 0) {  // compressed
-    int i = u;
+    src = &p.comp;
+    i = u;
     if (p.idx) {
-      const int32_t e = __ldg(p.idx + size_t(s.c0 + s.g) * p.k + i);
-      if (e >= ctl->n_min) set_status(p.status, DSV4KV_DEV_BAD_INDEX);
-      i = e >= ctl->n_min ? -1 : e;
+      const int n = entries(ctl->node_pos, p.window, p.stride);
+      i = u < min(p.k, n) ? __ldg(p.idx + size_t(s.c0 + s.g) * p.k + u) : -1;
+      if (i >= n) {
+        set_status(p.status, DSV4KV_DEV_BAD_INDEX);
+        i = -1;
+      }
     } else if (T >= s.full) {
-      key->lo = p.window + p.stride * (i + 1);  // N(p) > i
+      key->lo = p.window + p.stride * (u + 1);  // N(p) > u
+      if (key->lo > ctl->p_max) i = -1;
     }
-    if (i >= 0) *row = map_row(p.comp, s.b, i, p.status);
-    if (*row < 0) key->lo = kNever;
-    return *row < 0 ? nullptr : &p.comp;
-  }
-  if (j < s.w) {  // window row j holds the last position congruent to j
+  } else if (j < s.w) {  // window row j holds the last position congruent to j
+    src = &p.win;
+    i = j;
     key->hi = s.t - 1 - (s.t - 1 - j) % p.window + p.window;
-    if (!p.idx || key->hi >= ctl->node_pos) *row = map_row(p.win, s.b, j, p.status);
-    if (p.idx) key->hi = kNever;
-    if (*row < 0) key->lo = kNever;
-    return *row < 0 ? nullptr : &p.win;
+    if (p.idx) {
+      if (key->hi < ctl->node_pos) i = -1;
+      key->hi = kNever;
+    }
+  } else if (j - s.w < s.m) {
+    src = &p.draft;
+    i = j - s.w;
+    if (!p.idx) key->lo = -1 - i;
+    else if (!((ctl->anc[0][i >> 5] >> (i & 31)) & 1u)) i = -1;
+    if (i >= 0) i += s.c0;
   }
-  const int d = j - s.w;
-  key->lo = kNever;
-  if (d >= s.m || (p.idx && !((ctl->anc[0][d >> 5] >> (d & 31)) & 1u))) return nullptr;
-  if (!p.idx) key->lo = -1 - d;
-  else key->lo = 0;
-  *row = s.c0 + d;
-  return &p.draft;
+  *row = i >= 0 ? map_row(*src, s.b, i, p.status) : -1;
+  if (*row < 0) {
+    key->lo = kNever;
+    src = nullptr;
+  }
+  return src;
 }
 
 // ---------------------------------------------------------------- loader warps
@@ -325,59 +345,67 @@ __host__ __device__ constexpr int row_bytes(int fmt) {
                                       : kDim + 64;
 }
 
-// Dequantises channels [ch0, ch0 + kCh) of the warp's rows (row `rbase` + i is lane i's `my`; kR <= 32) to f16 in
-// 16-byte units of codes: 16 fp8 channels, 32 fp4 channels, or 8 bf16 rotary channels (stored as f16 of value /
-// scale: the row's scale is in the weights).  Four units a lane are loaded while the four before are converted.
-template <int FMT, int kR, int kCh, class Cell>
-__device__ __forceinline__ void dequant(const uint8_t* my, const uint8_t* mysc, float my_inv, int ch0, int lane, Cell cell) {
-  constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16, kFp4 = FMT == DSV4KV_FP4_E2M1_G16;
+// Dequantises channels [ch0, ch0 + 256) of kR <= 32 rows (row i is lane i's `my`) to f16, in units of 16 bytes of codes:
+// 16 fp8 channels, 32 fp4 channels, or 8 bf16 rotary channels (stored as f16 of value / scale: the row's scale is in the
+// weights).  A batch is 8 units a lane: fetch() issues its loads, put() converts it.
+template <int FMT, int kR>
+struct Dequant {
+  static constexpr bool kFp4 = FMT == DSV4KV_FP4_E2M1_G16;
+  [[maybe_unused]] static constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16;
+  static constexpr int kN = 8;
+  uint4 raw[kN];
+  uint32_t sc[kFp4 ? kN : 1];
+
   // units of a row: code units, then (where the channels reach the rotary ones) rotary units
-  const int body = kFp4 ? kCh / 32 : kRope ? (min(ch0 + kCh, kDim - 64) - ch0) / 16 : kCh / 16;
-  const int upr = kRope && ch0 + kCh > kDim - 64 ? body + 8 : body;
-  const int n = kR * upr;  // a multiple of 32
-  uint4 raw[2][4];
-  uint32_t sc[2][kFp4 ? 4 : 1];
-  auto fetch = [&](int at, uint4 (&v)[4], uint32_t (&s)[kFp4 ? 4 : 1]) {
+  static __device__ __forceinline__ int body(int ch0) {
+    return kFp4 ? kHalf / 32 : kRope && ch0 + kHalf > kDim - 64 ? (kDim - 64 - ch0) / 16 : kHalf / 16;
+  }
+  static __device__ __forceinline__ int per_row(int ch0) {
+    return kRope && ch0 + kHalf > kDim - 64 ? body(ch0) + 8 : body(ch0);
+  }
+  static __device__ __forceinline__ int batches(int ch0) { return (kR * per_row(ch0) + 32 * kN - 1) / (32 * kN); }
+
+  __device__ __forceinline__ void fetch(const uint8_t* my, const uint8_t* mysc, int ch0, int batch, int lane) {
+    const int bd = body(ch0), upr = per_row(ch0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int x = at + 32 * i + lane, r = min(x / upr, kR - 1), u = x - r * upr;
-      const uint8_t* row = shfl_ptr(my, r);
-      v[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kN; ++i) {
+      const int x = 32 * (kN * batch + i) + lane, r = x / upr, u = x - r * upr;
+      const uint8_t* row = shfl_ptr(my, min(r, kR - 1));
+      const bool in = r < kR && row;
+      raw[i] = in ? ld_stream_v4(row + (kFp4 ? ch0 / 2 + 16 * u : kRope && u >= bd ? kDim - 64 + 16 * (u - bd) : ch0 + 16 * u))
+                  : make_uint4(0, 0, 0, 0);
       if constexpr (kFp4) {
-        const uint8_t* srow = shfl_ptr(mysc, r);
-        s[i] = 0;
-        if (x < n && row) {
-          v[i] = ld_stream_v4(row + ch0 / 2 + 16 * u);
-          s[i] = *reinterpret_cast<const uint16_t*>(srow + ch0 / 16 + 2 * u);
-        }
-      } else {
-        if (x < n && row) v[i] = ld_stream_v4(row + (kRope && u >= body ? kDim - 64 + 16 * (u - body) : ch0 + 16 * u));
+        const uint8_t* srow = shfl_ptr(mysc, min(r, kR - 1));
+        sc[i] = in ? *reinterpret_cast<const uint16_t*>(srow + ch0 / 16 + 2 * u) : 0u;
       }
     }
-  };
-  auto put = [&](int at, const uint4 (&v)[4], const uint32_t (&s)[kFp4 ? 4 : 1]) {
+  }
+  // cell(row, channel - ch0): where 8 channels go
+  template <class Cell>
+  __device__ __forceinline__ void put(float my_inv, int ch0, int batch, int lane, Cell cell) const {
+    const int bd = body(ch0), upr = per_row(ch0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int x = at + 32 * i + lane, r = min(x / upr, kR - 1), u = x - r * upr;
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int i = 0; i < kN; ++i) {
+      const int x = 32 * (kN * batch + i) + lane, r = x / upr, u = x - r * upr;
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       float inv = 1.f;
-      if constexpr (kRope) inv = __shfl_sync(kFull, my_inv, r);
-      if (x >= n) continue;
+      if constexpr (kRope) inv = __shfl_sync(kFull, my_inv, min(r, kR - 1));
+      if (r >= kR) continue;
       if constexpr (kFp4) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t s1 = e < 2 ? s[i] & 0xffu : s[i] >> 8;
+          const uint32_t s1 = e < 2 ? sc[i] & 0xffu : sc[i] >> 8;
           const uint32_t s2 = e4m3x2_to_f16x2(s1 | (s1 << 8));
           uint32_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[j] = hmul2(e2m1x2_to_f16x2((w[e] >> (8 * j)) & 0xffu), s2);
           *reinterpret_cast<uint4*>(cell(r, 32 * u + 8 * e)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
-      } else if (kRope && u >= body) {
+      } else if (kRope && u >= bd) {
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = f32x2_to_f16x2_sat(bf16lo(w[e]) * inv, bf16hi(w[e]) * inv);
-        *reinterpret_cast<uint4*>(cell(r, kDim - 64 - ch0 + 8 * (u - body))) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(cell(r, kDim - 64 - ch0 + 8 * (u - bd))) = make_uint4(h[0], h[1], h[2], h[3]);
       } else {
         uint32_t h[8];
 #pragma unroll
@@ -389,16 +417,8 @@ __device__ __forceinline__ void dequant(const uint8_t* my, const uint8_t* mysc, 
         *reinterpret_cast<uint4*>(cell(r, 16 * u + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
     }
-  };
-  fetch(0, raw[0], sc[0]);
-#pragma unroll 1
-  for (int at = 0; at < n; at += 256) {
-    fetch(at + 128, raw[1], sc[1]);
-    put(at, raw[0], sc[0]);
-    fetch(at + 256, raw[0], sc[0]);
-    put(at + 128, raw[1], sc[1]);
   }
-}
+};
 
 // A tail tile in which some score is not finite: if row r's values are not finite the row is zeroed, so that its zero
 // weights (queries that do not see it) add zeros.  A query that is not finite itself says nothing.
@@ -420,10 +440,11 @@ __device__ __noinline__ void zero_bad_row(uint8_t* sV, int r) {
 
 // ---------------------------------------------------------------- the kernel
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_key,
-                const __grid_constant__ CUtensorMap tm_val, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_comp,
+                const __grid_constant__ Params p) {
   using C = Cfg<FMT>;
+  constexpr int kSoftThreads = C::kSoftThreads, kCols = C::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -438,18 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
 
   if (tid == 0) {
-    mbar_init(&ctl->q_ready, C::kQuant ? 2 * kSoftWarps : 1);
-    mbar_init(&ctl->k_full, 2 * kKeyWarps);
-    mbar_init(&ctl->v_full, 2 * kValWarps);
-    mbar_init(&ctl->p_full, 2 * kSoftWarps);
+    mbar_init(&ctl->q_ready, C::kQuant ? 2 * C::kSoftWarps : 1);
     mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->info[0], kValWarps);
-    mbar_init(&ctl->info[1], kValWarps);
-    mbar_init(&ctl->v_here, kValWarps);
-    mbar_init(&ctl->s_full[0], 1);
-    mbar_init(&ctl->s_full[1], 1);
-    mbar_init(&ctl->k_empty, 1);
-    mbar_init(&ctl->v_empty, 1);
+    mbar_init(&ctl->meta, C::kSoftWarps);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&ctl->k_full[x], 2 * kKeyWarps);
+      mbar_init(&ctl->v_full[x], C::kValWarps);
+      mbar_init(&ctl->p_full[x], C::kSoftWarps);
+      mbar_init(&ctl->info[x], C::kValWarps);
+      mbar_init(&ctl->v_here[x], C::kValWarps / 2);
+      mbar_init(&ctl->s_full[x], 1);
+      mbar_init(&ctl->k_empty[x], 1);
+      mbar_init(&ctl->v_empty[x], 1);
+    }
     mbar_init(&ctl->o_done, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -460,17 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
   if (tid == 64) {
     prefetch_tmap(&tm_q);
-    if (!C::kQuant) {
-      prefetch_tmap(&tm_key);
-      prefetch_tmap(&tm_val);
-    }
+    if (!C::kQuant) prefetch_tmap(&tm_comp);
   }
   tc_fence_before();
   pdl_wait();
 
   // ---- the batch: groups and tiles of every sequence (in the weights' place), then which part is this pair's
   int* tiles = reinterpret_cast<int*>(sP);
-  for (int b = tid; b < p.batch; b += kThreads) {
+  for (int b = tid; b < p.batch; b += C::kThreads) {
     int c0, m;
     uint32_t* st = blockIdx.x == 0 ? p.status : nullptr;
     seq_nodes(p, b, &c0, &m, st);
@@ -505,12 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ctl->share = share;
       ctl->units = u;
     }
-    const unsigned want = whole ? unsigned(pair) : unsigned(share) * unsigned(pair);
+    const unsigned want = unsigned(share) * unsigned(pair);
     unsigned at = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    for (int b0 = 0; b0 < p.batch && !whole; b0 += 32) {
       const int b = b0 + lane;
       const unsigned tl = b < p.batch ? tiles[b] : 0;
-      const unsigned v = b < p.batch ? unsigned(ctl->gpre[b + 1] - ctl->gpre[b]) * (whole ? 1u : tl) : 0u;
+      const unsigned v = b < p.batch ? unsigned(ctl->gpre[b + 1] - ctl->gpre[b]) * tl : 0u;
       unsigned x = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -519,154 +538,129 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const unsigned ex = at + x - v;
       if (want >= ex && want - ex < v) {
-        const unsigned off = want - ex;
         ctl->b = b;
-        ctl->g = whole ? off : off / tl;
-        ctl->t0 = whole ? 0 : off % tl;
+        ctl->g = (want - ex) / tl;
+        ctl->t0 = (want - ex) % tl;
       }
       at += __shfl_sync(kFull, x, 31);
     }
   }
+  if (tid < 2 && rank == 0) p.rec[2 * pair + tid].valid = 0;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const bool whole = ctl->whole != 0;
-  const int G = ctl->gpre[p.batch];
-  // (equal runs) tiles of this pair's run; (whole groups) the flattened group to take next
+  // Every warp walks the pair's parts by itself, so that the loads and scores of the next part run during this one's
+  // epilogue.  (equal runs) `left` tiles from (b, g, t0) on; (whole groups) flattened group `g_next`.
   int left = int(max(0ll, min((long long)ctl->share, ctl->units - (long long)ctl->share * pair)));
   int g_next = pair;
-  if (tid < 2 && rank == 0) p.rec[2 * pair + tid].valid = 0;
-
-  int cnt = 0, segs = 0;  // tiles and groups worked on so far: the barriers' phases
-  while (whole ? g_next < G : left > 0) {
-    // ---- the group: its rows, its nodes and their ancestors
-    Seg s;
-    s.b = ctl->b;
-    s.g = ctl->g;
-    s.t0 = ctl->t0;
-    seq_nodes(p, s.b, &s.c0, &s.m, nullptr);
-    s.t = seq_len(p, s.b, nullptr);
-    s.w = min(s.t, p.window);
-    s.tiles = tiles_of(p, entries(s.t + s.m - 1, p.window, p.stride), s.w, s.m);
-    s.t1 = whole ? s.tiles : min(s.tiles, s.t0 + left);
-    int first, last;  // nodes of the whole group
-    if (p.idx) {
-      const int hs = (p.heads + 1) / 2;  // the node's heads, half in each CTA
-      first = last = s.node0 = s.g;
-      s.n_nodes = 1;
-      s.row0 = (s.c0 + s.g) * p.heads + rank * hs;
-      s.rows = rank ? p.heads - hs : hs;
+  Seg s;
+  s.b = ctl->b;
+  s.g = ctl->g;
+  s.t0 = s.t1 = ctl->t0;
+  int cnt = 0, segs = -1;  // tiles and parts done so far: the barriers' phases
+  auto next_part = [&]() -> bool {
+    const int done = s.t1 - s.t0;  // (0 before the first part)
+    if (whole) {
+      if (g_next >= ctl->gpre[p.batch]) return false;
+      s.b = find_seq(ctl->gpre, p.batch, g_next);
+      s.g = g_next - ctl->gpre[s.b];
+      s.t0 = 0;
+      g_next += P;
     } else {
-      const int f = kGroup * s.g, all = min(kGroup, s.m * p.heads - f);
-      first = f / p.heads;
-      last = (f + all - 1) / p.heads;
-      s.rows = min(kQ, max(0, all - rank * kQ));
-      s.row0 = s.c0 * p.heads + f + rank * kQ;
-      s.node0 = (f + rank * kQ) / p.heads;
-      s.n_nodes = s.rows > 0 ? (f + rank * kQ + s.rows - 1) / p.heads - s.node0 + 1 : 0;
-    }
-    if (tid == 0) {
-      // the queries (the previous group's products have read theirs): on the first CTA's barrier, or, to be converted
-      // first, on this one's
-      const uint32_t bar = C::kQuant ? smem_u32(&ctl->q_full) : lead_addr(&ctl->q_ready);
-      if (C::kQuant) mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
-      else if (rank == 0) mbar_arrive_expect_tx(&ctl->q_ready, 2 * kQBytes);
-      tma_load_3d_pair(sQ, &tm_q, bar, 0, s.row0, 0);
-    }
-    if (tid == kThreads - 1) {
-      ctl->n_min = kNever;
-      ctl->n_max = 0;
-    }
-    if (tid < s.m) {  // (at most 256 nodes)
-      int par = p.parent[s.c0 + tid];
-      if (par < -1 || par >= tid) {
-        set_status(p.status, DSV4KV_DEV_BAD_TREE);
-        par = -1;
-      }
-      ctl->parent[tid] = int16_t(par);
-    }
-    for (int i = tid; i < kQ * (kMaxNodes / 32); i += kThreads) (&ctl->anc[0][0])[i] = 0;
-    if (tid < kQ) {
-      ctl->m[tid] = kNoMax;
-      ctl->row_node[tid] = 0;
-      ctl->row_pos[tid] = -1;
-    }
-    __syncthreads();
-    if (tid < s.m && tid >= first && tid <= last) {
-      int d = 0;
-      const int gj = tid - s.node0;
-      const bool mine = gj >= 0 && gj < s.n_nodes;
-      for (int j = ctl->parent[tid]; j >= 0; j = ctl->parent[j]) {
-        ++d;
-        if (mine) ctl->anc[gj][j >> 5] |= 1u << (j & 31);
-      }
-      const int pos = s.t + d, n = entries(pos, p.window, p.stride);
-      atomicMin(&ctl->n_min, n);
-      atomicMax(&ctl->n_max, n);
-      if (p.idx) ctl->node_pos = pos;
-      if (mine) {  // its query rows in this CTA
-        const int f = kGroup * s.g + rank * kQ;
-        const int lo = p.idx ? 0 : max(0, tid * p.heads - f), hi = p.idx ? s.rows : min(s.rows, (tid + 1) * p.heads - f);
-        for (int j = lo; j < hi; ++j) {
-          ctl->row_pos[j] = pos;
-          ctl->row_node[j] = uint8_t(gj);
+      left -= done;
+      if (left <= 0) return false;
+      if (segs >= 0) {
+        s.t0 = 0;
+        ++s.g;
+        while (s.g >= ctl->gpre[s.b + 1] - ctl->gpre[s.b]) {
+          ++s.b;
+          s.g = 0;
         }
       }
     }
-    __syncthreads();
-    s.n = p.idx ? min(p.k, ctl->n_min) : ctl->n_max;
-    s.full = p.idx ? 0 : ctl->n_min / kRows;
-    // (the deepest node may be less deep than the schedule allowed for: fewer tiles)
-    const int exact = (s.n + s.w + s.m + kRows - 1) / kRows;
-    const int nt = max(0, min(s.t1, exact) - s.t0);
+    cnt += done;
+    ++segs;
+    return true;
+  };
+  // (the two parts of a step: next_part() sets b, g, t0 and the phases; load_part() the rest)
+  auto load_part = [&]() {
+    seq_nodes(p, s.b, &s.c0, &s.m, nullptr);
+    s.t = seq_len(p, s.b, nullptr);
+    s.w = min(s.t, p.window);
+    const int n = entries(s.t + s.m - 1, p.window, p.stride);
+    s.tiles = tiles_of(p, n, s.w, s.m);
+    s.t1 = whole ? s.tiles : min(s.tiles, s.t0 + left);
+    s.n = p.idx ? min(p.k, n) : n;
+    s.full = p.idx ? 0 : entries(s.t, p.window, p.stride) / kRows;
+  };
 
-    if (warp == 1) {
-      // ---------------------------------------------------------- products (the first CTA issues them)
-      if (rank == 0) {
-        const uint32_t me = elect_lane();
-        uint64_t idle = 0;
-        auto stuck = [&]() {  // nothing was ready: bounded
-          const uint64_t now = globaltimer();
-          if (idle == 0) idle = now;
-          if (now - idle > kWaitLimitNs) *abort = 1;
-          return __any_sync(kFull, *abort != 0) != 0;
-        };
-        auto ready = [&](uint64_t* bar, uint32_t parity) {
-          return __all_sync(kFull, mbar_test_wait_cluster(bar, parity)) != 0;
-        };
-        bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------ queries
+    bool ok = true;
+    while (ok && next_part()) {
+      load_part();
+      const int row = p.idx ? (s.c0 + s.g) * p.heads + rank * ((p.heads + 1) / 2)
+                            : s.c0 * p.heads + kGroup * s.g + rank * kQ;
+      if (segs > 0) ok = warp_wait(&ctl->o_done, (segs - 1) & 1, abort, lane);  // (the last part's scores have read theirs)
+      if (ok && lane == 0) {
+        // on the first CTA's barrier, or, to be converted first, on this one's
+        if (C::kQuant) mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
+        else if (rank == 0) mbar_arrive_expect_tx(&ctl->q_ready, 2 * kQBytes);
+        tma_load_3d_pair(sQ, &tm_q, C::kQuant ? smem_u32(&ctl->q_full) : lead_addr(&ctl->q_ready), 0, row, 0);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products (the first CTA issues them)
+    if (rank == 0) {
+      const uint32_t me = elect_lane();
+      const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t pd = smem_desc_sw128(smem_u32(sP), 16, 1024);
+      const uint64_t vd = smem_desc_sw128(smem_u32(sV), kVSlab, 1024);
+      uint64_t idle = 0;
+      auto stuck = [&]() {  // nothing was ready: bounded
+        const uint64_t now = globaltimer();
+        if (idle == 0) idle = now;
+        if (now - idle > kWaitLimitNs) *abort = 1;
+        return __any_sync(kFull, *abort != 0) != 0;
+      };
+      auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_test_wait(bar, parity)) != 0; };
+      bool ok = true;
+      while (ok && next_part()) {
+        load_part();
+        const int nt = s.t1 - s.t0;
+        idle = 0;
         while (ok && !ready(&ctl->q_ready, segs & 1)) ok = !stuck();
-        const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t pd = smem_desc_sw128(smem_u32(sP), 16, 1024);
-        const uint64_t vd = smem_desc_sw128(smem_u32(sV), kVSlab, 1024);
-        int qk = 0, pv = 0;
+        int qk = 0, pv = 0;  // half tiles: 256 channels of the scores, 64 values of the output
         idle = 0;
 #pragma unroll 1
-        while (ok && pv < nt) {
-          if (pv < qk && ready(&ctl->p_full, (cnt + pv) & 1) && ready(&ctl->v_full, (cnt + pv) & 1)) {
+        while (ok && pv < 2 * nt) {
+          const int tq = cnt + (qk >> 1), tp = cnt + (pv >> 1);
+          if ((pv >> 1) < (qk >> 1) && ready(&ctl->p_full[pv & 1], tp & 1) && ready(&ctl->v_full[pv & 1], tp & 1)) {
             tc_fence_after();
+            const uint64_t ph = pd + ((pv & 1) * (kQSlab >> 4)), vh = vd + ((pv & 1) * (kVPart >> 4));
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int kr = 0; kr < kRows / 16; ++kr)
-                mma_f16_pair(me, tmem + kColO + 128 * n, pd + (((kr >> 2) * kQSlab + (kr & 3) * 32) >> 4),
-                             vd + (((kr >> 2) * kVPart + (kr & 3) * 2048 + 2 * n * kVSlab) >> 4), C::kIdescPV,
-                             (pv > 0 || kr > 0) ? 1u : 0u);
-            mma_commit_pair(me, &ctl->v_empty);
+              for (int kr = 0; kr < 4; ++kr)
+                mma_f16_pair(me, tmem + kColO + 128 * n, ph + ((kr * 32) >> 4), vh + ((kr * 2048 + 2 * n * kVSlab) >> 4),
+                             C::kIdescPV, (pv > 0 || kr > 0) ? 1u : 0u);
+            mma_commit_pair(me, &ctl->v_empty[pv & 1]);
             ++pv;
             idle = 0;
-          } else if (qk < nt && qk < pv + 2 && ready(&ctl->k_full, (cnt + qk) & 1)) {
+          } else if (qk < 2 * nt && (qk >> 1) < (pv >> 1) + 2 && ready(&ctl->k_full[qk & 1], tq & 1)) {
             tc_fence_after();
-            const int sb = (cnt + qk) & 1;
+            const uint32_t d = tmem + kColS + 64 * (tq & 1), on = qk & 1;
+            const uint64_t qh = qd + (on * (4 * kQSlab >> 4)), kh = kd + (on * (4 * kKSlab >> 4));
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_f16_pair(me, tmem + kColS + 64 * sb, qd + ((c * kQSlab + kk * 32) >> 4),
-                             kd + ((c * kKSlab + kk * 32) >> 4), C::kIdescQK, (c | kk) ? 1u : 0u);
-            mma_commit_pair(me, &ctl->s_full[sb]);
-            mma_commit_pair(me, &ctl->k_empty);
+                mma_f16_pair(me, d, qh + ((c * kQSlab + kk * 32) >> 4), kh + ((c * kKSlab + kk * 32) >> 4), C::kIdescQK,
+                             (c | kk) ? 1u : on);
+            if (on) mma_commit_pair(me, &ctl->s_full[tq & 1]);
+            mma_commit_pair(me, &ctl->k_empty[on]);
             ++qk;
             idle = 0;
           } else {
@@ -676,20 +670,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_pair(me, &ctl->o_done);  // completes once every product issued so far has
         if (!ok) wait_drain(&ctl->o_done, segs & 1);
       }
-    } else if (warp >= kSoft0) {
-      // ---------------------------------------------------------- softmax, epilogue
-      // TMEM lane 64 h + j: query j against rows 64 h + .. (scores), channels 256 h + .. (output)
-      const int wq = warp & 3, cg = (warp - kSoft0) >> 2, h = wq >> 1;
-      const int j = 32 * (wq & 1) + lane;            // this thread's query
-      const int r0 = 64 * h + kCols * cg;            // its first row of a tile
-      const uint32_t lane_base = uint32_t(32 * wq) << 16;
-      const int q = tid - 32 * kSoft0;  // (q < 64) the query that this thread keeps the statistics of
-      const bool live = j < s.rows;
+    }
+  } else if (warp >= C::kSoft0) {
+    // ------------------------------------------------------------ softmax, epilogue
+    // TMEM lane 64 h + j: query j against rows 64 h + .. (scores), channels 256 h + .. (output)
+    const int wq = warp & 3, cg = (warp - C::kSoft0) >> 2, h = wq >> 1;
+    const int j = 32 * (wq & 1) + lane;            // this thread's query
+    const int r0 = 64 * h + kCols * cg;            // its first row of a tile
+    const uint32_t lane_base = uint32_t(32 * wq) << 16;
+    const int q = tid - 32 * C::kSoft0;  // (q < 64) the query that this thread keeps the statistics of
+    bool dead = false;  // after a wait gave up: skips every access, still takes part in the group's barriers
+    while (next_part()) {
+      load_part();
+      const int nt = s.t1 - s.t0;
+      // ---- the group's nodes: [first, last], of them node0 .. node0 + n_nodes - 1 have query rows in this CTA
+      int first, last, node0, n_nodes, row0, rows;
+      const int f = kGroup * s.g + rank * kQ;  // first query row within the sequence
+      if (p.idx) {
+        const int hs = (p.heads + 1) / 2;  // the node's heads, half in each CTA
+        first = last = node0 = s.g;
+        n_nodes = 1;
+        row0 = (s.c0 + s.g) * p.heads + rank * hs;
+        rows = rank ? p.heads - hs : hs;
+      } else {
+        const int all = min(kGroup, s.m * p.heads - kGroup * s.g);
+        first = kGroup * s.g / p.heads;
+        last = (kGroup * s.g + all - 1) / p.heads;
+        rows = min(kQ, max(0, all - rank * kQ));
+        row0 = s.c0 * p.heads + f;
+        node0 = f / p.heads;
+        n_nodes = rows > 0 ? (f + rows - 1) / p.heads - node0 + 1 : 0;
+      }
+      for (int i = q; i < s.m; i += kSoftThreads) {
+        int par = p.parent[s.c0 + i];
+        if (par < -1 || par >= i) {
+          set_status(p.status, DSV4KV_DEV_BAD_TREE);
+          par = -1;
+        }
+        ctl->parent[i] = int16_t(par);
+      }
+      for (int i = q; i < kQ * (kMaxNodes / 32); i += kSoftThreads) (&ctl->anc[0][0])[i] = 0;
+      if (q < kQ) {
+        ctl->m[q] = kNoMax;
+        ctl->row_node[q] = 0;
+        ctl->row_pos[q] = -1;
+      }
+      if (q == kQ) ctl->p_max = 0;
+      soft_sync<kSoftThreads>();
+      for (int i = first + q; i <= last; i += kSoftThreads) {
+        int d = 0;
+        const int gj = i - node0;
+        const bool mine = gj >= 0 && gj < n_nodes;
+        for (int x = ctl->parent[i]; x >= 0; x = ctl->parent[x]) {
+          ++d;
+          if (mine) ctl->anc[gj][x >> 5] |= 1u << (x & 31);
+        }
+        const int at = s.t + d;
+        atomicMax(&ctl->p_max, at);
+        if (p.idx) ctl->node_pos = at;
+        if (mine) {  // its query rows in this CTA
+          const int lo = p.idx ? 0 : max(0, i * p.heads - f), hi = p.idx ? rows : min(rows, (i + 1) * p.heads - f);
+          for (int x = lo; x < hi; ++x) {
+            ctl->row_pos[x] = at;
+            ctl->row_node[x] = uint8_t(gj);
+          }
+        }
+      }
+      soft_sync<kSoftThreads>();
+      if (lane == 0) mbar_arrive(&ctl->meta);
+      const bool live = j < rows;
       const int pos = ctl->row_pos[j];
       const uint32_t* anc = ctl->anc[ctl->row_node[j]];
-      bool dead = false;
       if (C::kQuant) {  // queries to f16, in place
-        dead = !warp_wait(&ctl->q_full, segs & 1, abort, lane);
+        if (!dead) dead = !warp_wait(&ctl->q_full, segs & 1, abort, lane);
         if (!dead) {
 #pragma unroll 1
           for (int i = q; i < kQBytes / 16; i += kSoftThreads) {
@@ -701,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_addr(&ctl->q_ready));
+          if (lane == 0) mbar_arrive_pair(lead_addr(&ctl->q_ready));
         }
       }
       float l = 0.f;
@@ -710,9 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int T = s.t0 + i, c = cnt + i, sb = c & 1;
         if (!dead) dead = !warp_wait(&ctl->info[sb], (c >> 1) & 1, abort, lane);
         bool plain = true;
-        uint32_t seen = live ? 0xffffu : 0u;
+        uint32_t seen = live ? (kCols == 32 ? kFull : (1u << (kCols & 31)) - 1u) : 0u;
         if (!dead) {
-          plain = (ctl->plain[sb][0] & ctl->plain[sb][1]) == kFull;
+          uint32_t pl = kFull;
+#pragma unroll
+          for (int x = 0; x < C::kValWarps; ++x) pl &= ctl->plain[sb][x];
+          plain = pl == kFull;
           if (!plain && live) {
             seen = 0;
 #pragma unroll 4
@@ -732,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!dead) {
             tc_fence_after();
             uint32_t raw[kCols];
-            tmem_ld16(tmem + lane_base + kColS + 64 * sb + kCols * cg, raw);
+            tmem_ld_cols(tmem + lane_base + kColS + 64 * sb + kCols * cg, raw);
             tmem_wait_ld();
             const float m = ctl->m[j];
             if (!plain && again == 0 && T >= s.full) {
@@ -740,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int x = 0; x < kCols; ++x) odd |= (raw[x] & 0x7f800000u) == 0x7f800000u ? 1u << x : 0u;
               if (odd) {
-                wait_bar(&ctl->v_here, c & 1, abort);
+                wait_bar(&ctl->v_here[h], c & 1, abort);
                 for (int x = 0; x < kCols; ++x)
                   if ((odd >> x) & 1u) zero_bad_row<C::kQuant>(sV, r0 + x);
               }
@@ -756,33 +812,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kCols; ++x) d[x] -= m;
           }
-          if (again || !soft_or(raise)) break;
+          if (again || !soft_or<kSoftThreads>(raise)) break;
           ctl->part[2 * cg + h][j] = top;
-          soft_sync();
+          soft_sync<kSoftThreads>();
           if (q < kQ) {
             float mx = ctl->part[0][q];
 #pragma unroll
-            for (int x = 1; x < 8; ++x) mx = fmaxf(mx, ctl->part[x][q]);
+            for (int x = 1; x < 2 * C::kGroups; ++x) mx = fmaxf(mx, ctl->part[x][q]);
             const float m = ctl->m[q];
             const bool up = mx > m + kRaise;
             ctl->alpha[q] = up ? exp2_approx(m - mx) : 1.f;
             if (up) ctl->m[q] = mx;
           }
-          soft_sync();
+          soft_sync<kSoftThreads>();
           const float a = ctl->alpha[j];
           l *= a;
           if (i > 0) {  // the accumulator too, once the products before this tile's are in
-            if (!dead) dead = !warp_wait(&ctl->v_empty, (c - 1) & 1, abort, lane);
+            if (!dead) dead = !warp_wait(&ctl->v_empty[1], (c - 1) & 1, abort, lane);
             if (!dead) {
               tc_fence_after();
 #pragma unroll 1
-              for (int x = 0; x < 4; ++x) {
-                uint32_t o[kCols];
-                const uint32_t addr = tmem + lane_base + kColO + 64 * cg + kCols * x;
+              for (int x = 0; x < C::kChans; x += 16) {
+                uint32_t o[16];
+                const uint32_t addr = tmem + lane_base + kColO + C::kChans * cg + x;
                 tmem_ld16(addr, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < kCols; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
+                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
                 tmem_st16(addr, o);
               }
               tmem_wait_st();
@@ -805,262 +861,320 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += bf16lo(pk[x / 2]) + bf16hi(pk[x / 2]);
           }
         }
-        // the weights' buffer was last read by the previous tile's product
-        if (!dead && c > 0) dead = !warp_wait(&ctl->v_empty, (c - 1) & 1, abort, lane);
+        // this half of the weights was last read by the previous tile's product
+        if (!dead && c > 0) dead = !warp_wait(&ctl->v_empty[h], (c - 1) & 1, abort, lane);
         if (dead) continue;
         uint8_t* prow = sP + h * kQSlab + j * 128;
-        *reinterpret_cast<uint4*>(prow + (((2 * cg) ^ (j & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(prow + (((2 * cg + 1) ^ (j & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+#pragma unroll
+        for (int x = 0; x < kCols / 8; ++x)
+          *reinterpret_cast<uint4*>(prow + (((kCols / 8 * cg + x) ^ (j & 7)) << 4)) =
+              make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_addr(&ctl->p_full));
+        if (lane == 0) mbar_arrive_pair(lead_addr(&ctl->p_full[h]));
       }
       // ---- epilogue
-      soft_sync();  // (part is free: the last raise has been read)
+      soft_sync<kSoftThreads>();  // (part is free: the last raise has been read)
       ctl->part[2 * cg + h][j] = l;
       if (!dead) dead = !warp_wait(&ctl->o_done, segs & 1, abort, lane);
       tc_fence_after();
-      soft_sync();
+      // the rotations of the CTA's nodes, in the weights' place (the products have read them)
       const bool final_out = s.t0 == 0 && s.t1 == s.tiles;
+      const int pairs = p.rope_dim / 2;
+      float2* rot = reinterpret_cast<float2*>(sP);
+      const bool table = n_nodes * pairs <= kPBytes / 8;
+      if (!dead && final_out && table)
+        for (int x = q; x < n_nodes * pairs; x += kSoftThreads) {
+          const int node = x / pairs, at = p.idx ? 0 : max(0, (node0 + node) * p.heads - f);  // its first query row here
+          rotation(p.rope.theta_pi[x - node * pairs], ctl->row_pos[at], &rot[x].x, &rot[x].y);
+        }
+      soft_sync<kSoftThreads>();
       const int slot = 2 * pair + (s.t0 == 0 ? 1 : 0);
       if (!dead && q < kQ) {
         float L = 0.f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) L += ctl->part[x][q];
+        for (int x = 0; x < 2 * C::kGroups; ++x) L += ctl->part[x][q];
         ctl->alpha[q] = !final_out ? 1.f : L == 0.f ? 0.f : __frcp_rn(L);  // (no row: zeros)
         if (!final_out) {
           // (a query that is not finite: its NaN has to pass the merge, which skips runs without rows)
           p.ml[size_t(slot) * kGroup + rank * kQ + q] =
               make_float4(L != L ? INFINITY : ctl->m[q], L, __int_as_float(ctl->row_pos[q]),
-                          __int_as_float(q < s.rows ? s.row0 + q : -1));
+                          __int_as_float(q < rows ? row0 + q : -1));
           if (q == 0 && rank == 0) p.rec[slot] = Rec{1, s.b, s.g, s.t0, s.t1, s.tiles, 0, 0};
         }
       }
-      // the rotations of the CTA's nodes, in the queries' place (they have been read)
-      const int pairs = p.rope_dim / 2;
-      float2* rot = reinterpret_cast<float2*>(sQ);
-      const bool table = s.n_nodes * pairs <= kQBytes / 8;
-      if (!dead && final_out && table)
-        for (int x = q; x < s.n_nodes * pairs; x += kSoftThreads) {
-          const int node = x / pairs;
-          int at = 0;  // the node's position: that of its first query row here
-          if (!p.idx) at = max(0, (s.node0 + node) * p.heads - (kGroup * s.g + rank * kQ));
-          rotation(p.rope.theta_pi[x - node * pairs], ctl->row_pos[at], &rot[x].x, &rot[x].y);
-        }
-      soft_sync();
-      if (!dead && nt > 0) {
+      soft_sync<kSoftThreads>();
+      if (!dead) {
         const float a = ctl->alpha[j];
         const float2* my_rot = rot + ctl->row_node[j] * pairs;
-        const int rch = kDim - p.rope_dim;
+        const int rch = kDim - p.rope_dim, odd = lane & 1;
+        // lane pairs swap 16-byte pieces, so that a store fills whole 32-byte sectors: first the even lane's row
+        const bool live_e = (j & ~1) < rows, live_o = (j | 1) < rows;
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          const int ch = kHalf * h + 64 * cg + kCols * x;
-          uint32_t o[kCols];
-          tmem_ld16(tmem + lane_base + kColO + 64 * cg + kCols * x, o);
+        for (int x = 0; x < C::kChans; x += 16) {
+          const int ch = kHalf * h + C::kChans * cg + x;
+          uint32_t o[16];
+          tmem_ld16(tmem + lane_base + kColO + C::kChans * cg + x, o);
           tmem_wait_ld();
-          if (!live) continue;
-          float v[kCols];
 #pragma unroll
-          for (int y = 0; y < kCols; ++y) v[y] = a == 0.f ? 0.f : __uint_as_float(o[y]) * a;
-          if (!final_out) {
-            float4* dst = reinterpret_cast<float4*>(p.o_part + (size_t(slot) * kGroup + rank * kQ + j) * kDim + ch);
+          for (int y = 0; y < 16; ++y) o[y] = a == 0.f ? 0u : __float_as_uint(__uint_as_float(o[y]) * a);
+          if (final_out && ch + 16 > rch && live) {
 #pragma unroll
-            for (int y = 0; y < kCols / 4; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-            continue;
-          }
-          if (ch + kCols > rch) {
-#pragma unroll
-            for (int y = 0; y < kCols; y += 2) {
+            for (int y = 0; y < 16; y += 2) {
               if (ch + y < rch) continue;
               const int m = (ch + y - rch) >> 1;
               float2 r;
               if (table) r = my_rot[m];
               else rotation(p.rope.theta_pi[m], pos, &r.x, &r.y);
-              const float e = v[y], f = v[y + 1];
-              v[y] = fmaf(e, r.x, -f * r.y);
-              v[y + 1] = fmaf(e, r.y, f * r.x);
+              const float e = __uint_as_float(o[y]), g = __uint_as_float(o[y + 1]);
+              o[y] = __float_as_uint(fmaf(e, r.x, -g * r.y));
+              o[y + 1] = __float_as_uint(fmaf(e, r.y, g * r.x));
             }
           }
-          const size_t at = size_t(s.row0 + j) * kDim + ch;
-          if (p.out_fp32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+          if (final_out && !p.out_fp32) {
+            uint32_t w[8];
 #pragma unroll
-            for (int y = 0; y < kCols / 4; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+            for (int y = 0; y < 8; ++y) w[y] = cvt_bf16x2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]));
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // the even lane keeps both rows' first piece, the odd lane the second
+              const uint32_t got = __shfl_xor_sync(kFull, odd ? w[y] : w[4 + y], 1);
+              if (odd) w[y] = got;
+              else w[4 + y] = got;
+            }
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + size_t(row0 + (j & ~1)) * kDim + ch + 8 * odd;
+            if (live_e) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (live_o) *reinterpret_cast<uint4*>(dst + kDim) = make_uint4(w[4], w[5], w[6], w[7]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
 #pragma unroll
-            for (int y = 0; y < kCols / 8; ++y)
-              dst[y] = make_uint4(cvt_bf16x2(v[8 * y], v[8 * y + 1]), cvt_bf16x2(v[8 * y + 2], v[8 * y + 3]),
-                                  cvt_bf16x2(v[8 * y + 4], v[8 * y + 5]), cvt_bf16x2(v[8 * y + 6], v[8 * y + 7]));
+            for (int z = 0; z < 16; z += 8) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t got = __shfl_xor_sync(kFull, odd ? o[z + y] : o[z + 4 + y], 1);
+                if (odd) o[z + y] = got;
+                else o[z + 4 + y] = got;
+              }
+              float* dst = (final_out ? static_cast<float*>(p.out) + size_t(row0 + (j & ~1)) * kDim
+                                      : p.o_part + (size_t(slot) * kGroup + rank * kQ + (j & ~1)) * kDim) + ch + z + 4 * odd;
+              if (live_e) *reinterpret_cast<uint4*>(dst) = make_uint4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+              if (live_o) *reinterpret_cast<uint4*>(dst + kDim) = make_uint4(o[z + 4], o[z + 5], o[z + 6], o[z + 7]);
+            }
           }
         }
       }
-      fence_proxy_async_smem();  // (the next queries' copy overwrites the rotations)
-    } else if (warp >= kVal0) {
-      // ---------------------------------------------------------- values, and what the rows are
-      const int vw = warp - kVal0;
-      bool ok = true;
+      tc_fence_before();
+      soft_sync<kSoftThreads>();  // (the statistics and rotations are read; the next part overwrites them)
+    }
+  } else if (warp >= kVal0) {
+    // ------------------------------------------------------------ values, and what the rows are
+    const int vw = warp - kVal0, half = vw / (C::kValWarps / 2);
+    constexpr int kX = C::kValRows / 32;  // rows a lane
+    // tile T's rows of this warp: the one TMA row, or kX rows a lane
+    struct Set {
+      bool tma;
+      int32_t row0;
+      const uint8_t *my[kX], *mysc[kX];
+      float sr[kX];
+      Key key[kX];
+    };
+    int met = -1;  // the last part whose nodes were waited for
+    bool ok = true;
+    auto resolve = [&](Set& e, int T) {
+      int32_t trow[2];
+      e.tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
+      e.row0 = half ? trow[1] : trow[0];
+      if (e.tma) return;
+      if (T >= s.full && met != segs) {
+        ok = warp_wait(&ctl->meta, segs & 1, abort, lane);
+        met = segs;
+        if (!ok) return;
+      }
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        int64_t row;
+        const Rows* src = row_source(p, s, ctl, T, C::kValRows * vw + 32 * x + lane, &row, &e.key[x]);
+        e.my[x] = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
+        if (FMT == DSV4KV_FP4_E2M1_G16)
+          e.mysc[x] = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
+        if (C::kRowScale) e.sr[x] = src ? static_cast<const float*>(src->scales)[row] : 0.f;
+      }
+    };
+    while (ok && next_part()) {
+      load_part();
+      const int nt = s.t1 - s.t0;
+      Set cur, nxt;
+      Dequant<FMT, 32> dq;
+      resolve(cur, s.t0);
+      if (!ok) break;
+      if constexpr (C::kQuant) dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, 0, lane);
 #pragma unroll 1
       for (int i = 0; i < nt && ok; ++i) {
         const int T = s.t0 + i, c = cnt + i, sb = c & 1;
-        int32_t trow[2];
-        const bool tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
-        const uint8_t *my[2] = {nullptr, nullptr}, *mysc[2] = {nullptr, nullptr};
-        float inv[2] = {0.f, 0.f};
-        if (tma) {
+        float inv = 0.f;
+        // (the softmax is done with tile c - 2's: its product has been waited for)
+        if (cur.tma) {
           if (lane == 0) ctl->plain[sb][vw] = kFull;
         } else {
           uint32_t plain = kFull;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int r = 64 * vw + 32 * x + lane;
-            int64_t row;
-            Key key;
-            const Rows* src = row_source(p, s, ctl, T, r, &row, &key);
-            if (src) {
-              my[x] = src->codes + size_t(row) * row_bytes(FMT);
-              if (FMT == DSV4KV_FP4_E2M1_G16) mysc[x] = static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16);
-            }
+          for (int x = 0; x < kX; ++x) {
+            const int r = C::kValRows * vw + 32 * x + lane;
             if (C::kRowScale) {
-              const float sr = src ? static_cast<const float*>(src->scales)[row] : 0.f;
-              inv[x] = sr > 0.f ? __frcp_rn(sr) : 0.f;
+              const float sr = cur.sr[x];
+              inv = sr > 0.f ? __frcp_rn(sr) : 0.f;
               ctl->scale[sb][r] = sr;
               ctl->lscale[sb][r] = sr > 0.f ? __log2f(sr) : 0.f;
-              ctl->iscale[sb][r] = inv[x];
+              ctl->iscale[sb][r] = inv;
             }
-            ctl->key[sb][r] = key;
-            plain &= __ballot_sync(kFull, key.lo == 0 && key.hi == kNever);
+            ctl->key[sb][r] = cur.key[x];
+            plain &= __ballot_sync(kFull, cur.key[x].lo == 0 && cur.key[x].hi == kNever);
           }
           if (lane == 0) ctl->plain[sb][vw] = plain;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->info[sb]);
-        if (c > 0) ok = warp_wait(&ctl->v_empty, (c - 1) & 1, abort, lane);
+        if (i + 1 < nt) resolve(nxt, T + 1);  // (its table and index reads, while the buffer is in use)
+        if (ok && c > 0) ok = warp_wait(&ctl->v_empty[half], (c - 1) & 1, abort, lane);
         if (!ok) break;
-        if (tma) {
+        const uint32_t bar = lead_addr(&ctl->v_full[half]);
+        if (cur.tma) {
           if (lane == 0) {
-            const uint32_t bar = lead_addr(&ctl->v_full);
-            if (vw == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->v_full, 2 * kVBytes);
-            else mbar_arrive_cluster(bar);
-            if (vw == 0) {
-              tma_load_3d_pair(sV, &tm_val, bar, 0, trow[0], 4 * rank);
-              tma_load_3d_pair(sV + kVPart, &tm_val, bar, 0, trow[1], 4 * rank);
-            }
+            if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[half], 2 * kVPart);
+            else mbar_arrive_pair(bar);
+            tma_load_3d_pair(sV + half * kVPart, &tm_comp, bar, 0, cur.row0, 4 * rank);
+            mbar_arrive(&ctl->v_here[half]);  // (nobody waits for a whole tile's)
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->v_here);  // (nobody waits for a whole tile's)
-          continue;
-        }
+        } else {
+          if constexpr (C::kQuant) {
+            const int nb = dq.batches(kHalf * rank);
+            auto cell = [&](int r, int ch) { return val_cell(sV, C::kValRows * vw + r, ch); };
+            dq.put(inv, kHalf * rank, 0, lane, cell);
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const uint8_t *src = x ? my[1] : my[0], *ssrc = x ? mysc[1] : mysc[0];
-          const int rb = 64 * vw + 32 * x;
-          if constexpr (!C::kQuant) {
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r) {  // a row's 256 channels: 32 lanes of 16 bytes
-              const uint8_t* g = shfl_ptr(src, r);
-              cp_async16_zfill(val_cell(sV, rb + r, 8 * lane), g ? g + 2 * (kHalf * rank + 8 * lane) : p.draft.codes,
-                               g ? 16 : 0);
+            for (int x = 1; x < nb; ++x) {
+              dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, x, lane);
+              dq.put(inv, kHalf * rank, x, lane, cell);
             }
           } else {
-            dequant<FMT, 32, kHalf>(src, ssrc, x ? inv[1] : inv[0], kHalf * rank, lane,
-                                    [&](int r, int ch) { return val_cell(sV, rb + r, ch); });
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
+#pragma unroll 8
+              for (int r = 0; r < 32; ++r) {  // a row's 256 channels: 32 lanes of 16 bytes
+                const uint8_t* g = shfl_ptr(cur.my[x], r);
+                cp_async16_zfill(val_cell(sV, C::kValRows * vw + 32 * x + r, 8 * lane),
+                                 g ? g + 2 * (kHalf * rank + 8 * lane) : p.draft.codes, g ? 16 : 0);
+              }
+            cp_async_commit();
+            cp_async_wait_group<0>();
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl->v_here[half]);
+            mbar_arrive_pair(bar);
           }
         }
-        if constexpr (!C::kQuant) {
-          cp_async_commit();
-          cp_async_wait_group<0>();
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->v_here);
-          mbar_arrive_cluster(lead_addr(&ctl->v_full));
-        }
+        cur = nxt;
+        if constexpr (C::kQuant)
+          if (i + 1 < nt) dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, 0, lane);
       }
-    } else if (warp >= kKey0) {
-      // ---------------------------------------------------------- keys
-      const int kw = warp - kKey0;
-      bool ok = true;
+    }
+  } else {
+    // ------------------------------------------------------------ keys (16 rows a warp), 256 channels at a time
+    const int kw = warp - kKey0;
+    struct Set {
+      bool tma;
+      int32_t row0;
+      const uint8_t *my, *mysc;
+      float inv;
+    };
+    int met = -1;
+    bool ok = true;
+    auto resolve = [&](Set& e, int T) {
+      int32_t trow[2];
+      e.tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
+      e.row0 = rank ? trow[1] : trow[0];
+      if (e.tma) return;
+      if (T >= s.full && met != segs) {
+        ok = warp_wait(&ctl->meta, segs & 1, abort, lane);
+        met = segs;
+        if (!ok) return;
+      }
+      int64_t row;
+      Key key;
+      const Rows* src = row_source(p, s, ctl, T, kKeys * rank + 16 * kw + (lane & 15), &row, &key);
+      e.my = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
+      if (FMT == DSV4KV_FP4_E2M1_G16)
+        e.mysc = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
+      if (C::kRowScale) {
+        const float sr = src ? static_cast<const float*>(src->scales)[row] : 0.f;
+        e.inv = sr > 0.f ? __frcp_rn(sr) : 0.f;
+      }
+    };
+    while (ok && next_part()) {
+      load_part();
+      const int nt = s.t1 - s.t0;
+      Set cur, nxt;
+      Dequant<FMT, 16> dq;
+      resolve(cur, s.t0);
+      if (!ok) break;
+      if constexpr (C::kQuant) dq.fetch(cur.my, cur.mysc, 0, 0, lane);
 #pragma unroll 1
       for (int i = 0; i < nt && ok; ++i) {
         const int T = s.t0 + i, c = cnt + i;
-        int32_t trow[2];
-        const bool tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
-        const uint8_t *my = nullptr, *mysc = nullptr;
-        float inv = 0.f;
-        if (!tma) {
-          int64_t row;
-          Key key;
-          const Rows* src = row_source(p, s, ctl, T, kKeys * rank + 16 * kw + (lane & 15), &row, &key);
-          if (src) {
-            my = src->codes + size_t(row) * row_bytes(FMT);
-            if (FMT == DSV4KV_FP4_E2M1_G16) mysc = static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16);
-            if (C::kRowScale) {
-              const float sr = static_cast<const float*>(src->scales)[row];
-              inv = sr > 0.f ? __frcp_rn(sr) : 0.f;
+        if (i + 1 < nt) resolve(nxt, T + 1);  // (its table and index reads, while the buffer is in use)
+#pragma unroll 1
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (c > 0) ok = warp_wait(&ctl->k_empty[x], (c - 1) & 1, abort, lane);
+          if (!ok) break;
+          const uint32_t bar = lead_addr(&ctl->k_full[x]);
+          if (cur.tma) {
+            if (lane == 0) {
+              if (kw == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->k_full[x], kKBytes);
+              else mbar_arrive_pair(bar);
+              if (kw == 0) tma_load_3d_pair(sK + 4 * x * kKSlab, &tm_comp, bar, 0, cur.row0, 4 * x);
+            }
+            __syncwarp();
+            continue;
+          }
+          if constexpr (!C::kQuant) {
+#pragma unroll 8
+            for (int r = 0; r < 16; ++r) {  // a row's 256 channels: 32 lanes of 16 bytes
+              const uint8_t* g = shfl_ptr(cur.my, r);
+              const int ch = kHalf * x + 8 * lane;
+              cp_async16_zfill(key_cell(sK, 16 * kw + r, ch), g ? g + 2 * ch : p.draft.codes, g ? 16 : 0);
+            }
+            cp_async_commit();
+            if (x == 0) continue;  // (handed over below, while the second half is on its way)
+            cp_async_wait_group<1>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead_addr(&ctl->k_full[0]));
+            cp_async_wait_group<0>();
+          } else {
+            auto cell = [&](int r, int ch) { return key_cell(sK, 16 * kw + r, kHalf * x + ch); };
+            const int nb = dq.batches(kHalf * x);
+            dq.put(cur.inv, kHalf * x, 0, lane, cell);
+#pragma unroll 1
+            for (int y = 1; y < nb; ++y) {
+              dq.fetch(cur.my, cur.mysc, kHalf * x, y, lane);
+              dq.put(cur.inv, kHalf * x, y, lane, cell);
             }
           }
-        }
-        if (c > 0) ok = warp_wait(&ctl->k_empty, (c - 1) & 1, abort, lane);
-        if (!ok) break;
-        const uint32_t bar = lead_addr(&ctl->k_full);
-        if (tma) {
-          if (lane == 0) {
-            if (kw == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->k_full, 2 * kKBytes);
-            else mbar_arrive_cluster(bar);
-            if (kw == 0) tma_load_3d_pair(sK, &tm_key, bar, 0, rank ? trow[1] : trow[0], 0);
-          }
+          fence_proxy_async_smem();
           __syncwarp();
-          continue;
+          if (lane == 0) mbar_arrive_pair(bar);
+          if constexpr (C::kQuant)
+            if (x == 0) dq.fetch(cur.my, cur.mysc, kHalf, 0, lane);
         }
-        if constexpr (!C::kQuant) {
-#pragma unroll 8
-          for (int x = 0; x < 32; ++x) {  // half a row's 512 channels: 32 lanes of 16 bytes
-            const int r = x >> 1, ch = kHalf * (x & 1) + 8 * lane;
-            const uint8_t* g = shfl_ptr(my, r);
-            cp_async16_zfill(key_cell(sK, 16 * kw + r, ch), g ? g + 2 * ch : p.draft.codes, g ? 16 : 0);
-          }
-          cp_async_commit();
-          cp_async_wait_group<0>();
-        } else {
-          dequant<FMT, 16, kDim>(my, mysc, inv, 0, lane, [&](int r, int ch) { return key_cell(sK, 16 * kw + r, ch); });
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(bar);
+        if (!ok) cp_async_wait_group<0>();
+        cur = nxt;
+        if constexpr (C::kQuant)
+          if (ok && i + 1 < nt) dq.fetch(cur.my, cur.mysc, 0, 0, lane);
       }
     }
-    cnt += nt;
-    ++segs;
-    if (whole) g_next += P;
-    else left -= s.t1 - s.t0;
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (ctl->abort) break;
-    // ---- the next part
-    if (whole) {
-      for (int b = tid; b < p.batch; b += kThreads)
-        if (ctl->gpre[b] <= g_next && g_next < ctl->gpre[b + 1]) {
-          ctl->b = b;
-          ctl->g = g_next - ctl->gpre[b];
-          ctl->t0 = 0;
-        }
-    } else if (tid == 0 && left > 0) {
-      int b = s.b, g = s.g + 1;
-      while (b < p.batch && g >= ctl->gpre[b + 1] - ctl->gpre[b]) {
-        ++b;
-        g = 0;
-      }
-      ctl->b = b;
-      ctl->g = g;
-      ctl->t0 = 0;
-    }
-    __syncthreads();
   }
+  __syncthreads();
   if (ctl->abort) {
     if (tid == 0) set_status(p.status, DSV4KV_DEV_TIMEOUT);
     // copies that were in flight when a wait gave up have landed long before this
@@ -1165,8 +1279,7 @@ Layout layout(int P) {
 }
 
 template <int FMT>
-cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int P,
-                        cudaStream_t stream) {
+cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tc, const Params& p, int P, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
   if (!done_on_device(ready)) {
     const cudaError_t e =
@@ -1174,7 +1287,8 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     if (e != cudaSuccess) return e;
     mark_done_on_device(ready);
   }
-  return launch_pdl_cluster(tree_kernel<FMT>, dim3(unsigned(2 * P)), dim3(kThreads), kSmemBytes, 2, stream, tq, tk, tv, p);
+  return launch_pdl_cluster(tree_kernel<FMT>, dim3(unsigned(2 * P)), dim3(Cfg<FMT>::kThreads), kSmemBytes, 2, stream, tq, tc,
+                            p);
 }
 
 Rows rows_of(const dsv4kv_cache& c, const PageDesc& pg) {
@@ -1220,23 +1334,21 @@ dsv4kv_status tree_decode_launch(const TreeArgs& a, void* ws, cudaStream_t strea
   p.ml = reinterpret_cast<float4*>(base + lay.ml);
   p.o_part = reinterpret_cast<float*>(base + lay.o);
   rope_table_fill(&p.rope, a.rope_dim, a.rope_base);
-  // boxes of 64 rows x 8 (queries, keys) or 4 (values) chunks of 64 channels, chunk after chunk in shared memory
-  CUtensorMap tq{}, tk{}, tv{};
+  // boxes of 64 rows x 8 (queries) or 4 (keys, values) chunks of 64 channels, chunk after chunk in shared memory
+  CUtensorMap tq{}, tc{};
   if (!encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 64, uint64_t(a.nodes) * a.heads, 8, kDim * 2, 128, 64, kQ,
                       8, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(DSV4KV_ERR_CUDA, "tree_decode_paged: tensor map of q");
   if (a.comp.fmt == DSV4KV_BF16 && a.comp.codes &&
-      (!encode_tmap_3d(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, 64, uint64_t(a.comp.rows), 8, kDim * 2, 128, 64,
-                       kKeys, 8, CU_TENSOR_MAP_SWIZZLE_128B) ||
-       !encode_tmap_3d(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, 64, uint64_t(a.comp.rows), 8, kDim * 2, 128, 64,
-                       64, 4, CU_TENSOR_MAP_SWIZZLE_128B)))
+      !encode_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, 64, uint64_t(a.comp.rows), 8, kDim * 2, 128, 64,
+                      64, 4, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(DSV4KV_ERR_CUDA, "tree_decode_paged: tensor map of the compressed cache");
   cudaError_t e;
   switch (a.comp.fmt) {
-    case DSV4KV_BF16: e = launch_tree<DSV4KV_BF16>(tq, tk, tv, p, P, stream); break;
-    case DSV4KV_FP8_E4M3_ROW: e = launch_tree<DSV4KV_FP8_E4M3_ROW>(tq, tk, tv, p, P, stream); break;
-    case DSV4KV_FP4_E2M1_G16: e = launch_tree<DSV4KV_FP4_E2M1_G16>(tq, tk, tv, p, P, stream); break;
-    default: e = launch_tree<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(tq, tk, tv, p, P, stream); break;
+    case DSV4KV_BF16: e = launch_tree<DSV4KV_BF16>(tq, tc, p, P, stream); break;
+    case DSV4KV_FP8_E4M3_ROW: e = launch_tree<DSV4KV_FP8_E4M3_ROW>(tq, tc, p, P, stream); break;
+    case DSV4KV_FP4_E2M1_G16: e = launch_tree<DSV4KV_FP4_E2M1_G16>(tq, tc, p, P, stream); break;
+    default: e = launch_tree<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(tq, tc, p, P, stream); break;
   }
   if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "tree_kernel: %s", cudaGetErrorString(e));
   dsv4kv_status st = check_launch("tree_kernel");
