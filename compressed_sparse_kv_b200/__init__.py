@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -107,19 +108,19 @@ _SIGS = {
                                              _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
                                              _c.c_void_p]),
     "dsv4kv_slot_map": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32,
-                                   _c.c_int32, _c.POINTER(PageTableDesc), _c.POINTER(PageTableDesc), _c.c_int64,
+                                   _c.c_int32, _c.c_void_p, _c.c_void_p, _c.c_int64,
                                    _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
                                    _c.c_size_t, _c.c_void_p]),
     "dsv4kv_append_paged": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int64, _c.c_void_p, _c.c_void_p,
                                        _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_int32, _c.c_int32,
                                        _c.c_int32, _c.c_int64, _c.c_int32, _c.c_double, _c.c_void_p,
-                                       _c.POINTER(PagedDesc), _c.POINTER(PagedDesc), _c.c_void_p, _c.c_size_t,
+                                       _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
                                        _c.c_void_p]),
     "dsv4kv_tree_decode_paged_workspace_bytes": (_c.c_size_t, [_c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32,
                                                                _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32,
                                                                _c.c_int32]),
-    "dsv4kv_tree_decode_paged": (_c.c_int, [_c.c_void_p, _c.POINTER(PagedDesc), _c.POINTER(PagedDesc),
-                                            _c.POINTER(CacheDesc), _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32,
+    "dsv4kv_tree_decode_paged": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                            _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int32,
                                             _c.c_int32, _c.c_int64, _c.c_int32, _c.c_void_p, _c.c_int64, _c.c_int32,
                                             _c.c_int32, _c.c_int32, _c.c_float, _c.c_int32, _c.c_double, _c.c_int32,
                                             _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
@@ -217,40 +218,89 @@ class SlotMap:
     comp_slot: torch.Tensor                  # int32 [capacity]
 
 
-def _need(t, dtype, shape, where: str, name: str, device) -> None:
-    """Refuse a tensor that is not dense, of that type and shape (None: any size) and on the call's device."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or any(
-            w is not None and w != g for g, w in zip(t.shape, shape)):
-        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor {list(shape)} on {device}, "
-                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+# The serving-step calls run once per layer and step, so their checks are written to cost well under a microsecond each:
+# every tensor is dense, of its type, on the call's device (its index) and of its shape.
+_I32, _I64, _F32, _BF, _U8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
+_PAGED = struct.Struct("@iiiiqPPP")   # dsv4kv_paged_cache
+_CACHE = struct.Struct("@iiqPP")      # dsv4kv_cache
+_TABLE = struct.Struct("@Piiq")       # dsv4kv_page_table
 
 
-def _on(device, stream):
+def _is(t, dtype, dev: int) -> bool:
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _refuse(t, dtype, shape: str, dev: int, where: str, name: str):
+    raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor {shape} on device {dev}, "
+                     f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _on(dev: int, stream, where: str):
     """(context, stream handle) of a call: on its tensors' device and `stream`, or that device's current stream; what
     the call allocates inside the context belongs to that stream."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    if dev < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != dev:
+            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on device {dev}")
         return torch.cuda.stream(stream), stream.cuda_stream
-    here = device.index == torch.cuda.current_device()
-    return contextlib.nullcontext() if here else torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    here = dev == torch.cuda.current_device()
+    return _HERE if here else torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
 
 
+_HERE = contextlib.nullcontext()
 _ROW_BYTES = {BF16: 1024, FP8_E4M3_ROW: 512, FP4_E2M1_G16: 256, FP8_E4M3_ROW_ROPE_BF16: 576}
+_SCALE_BYTES = {FP8_E4M3_ROW: 4, FP4_E2M1_G16: 32, FP8_E4M3_ROW_ROPE_BF16: 4}
 
 
-def _need_rows(c, rows, where: str, name: str, device) -> None:
-    """Refuse a 512-channel cache whose codes or scales are not dense, on the device and at least `rows` rows long."""
-    if c.dim != 512 or c.fmt not in _ROW_BYTES:
-        return                                # (the library's own refusal)
-    got = [("codes", c.codes, _ROW_BYTES[c.fmt])]
-    if c.fmt != BF16:
-        got.append(("scales", c.scales, 32 if c.fmt == FP4_E2M1_G16 else 4))
-    for what, t, per in got:
-        if t is None or t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < rows * per:
-            raise ValueError(f"{where}: {name}.{what} must be contiguous, on {device}, and hold {rows} rows")
+def _rows(c, rows: int, dev: int, where: str, name: str) -> tuple[int, int]:
+    """(codes, scales) of a 512-channel cache that holds at least `rows` rows, densely, on the device."""
+    t = c.codes
+    per = _ROW_BYTES.get(c.fmt, 0) if c.dim == 512 else 0      # (else: the library's own refusal)
+    if t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < rows * per:
+        raise ValueError(f"{where}: {name}.codes must be contiguous, on device {dev}, and hold {rows} rows")
+    if c.fmt == BF16:
+        return t.data_ptr(), 0
+    s = c.scales
+    if s is None or s.get_device() != dev or not s.is_contiguous() or (
+            per and s.numel() * s.element_size() < rows * _SCALE_BYTES[c.fmt]):
+        raise ValueError(f"{where}: {name}.scales must be contiguous, on device {dev}, and hold {rows} rows")
+    return t.data_ptr(), s.data_ptr()
+
+
+def _paged(c, b: int, dev: int, where: str, name: str) -> bytes:
+    """The descriptor of a paged cache of b sequences."""
+    t = c.table
+    if not (_is(t, _I32, dev) and t.dim() == 2 and t.shape[0] == b):
+        _refuse(t, _I32, f"[{b}, ...]", dev, where, name + ".table")
+    page, pages = c.page_rows, c.pool_pages
+    codes, scales = _rows(c, page * pages, dev, where, name)
+    return _PAGED.pack(c.fmt, c.dim, page, t.shape[1], pages, t.data_ptr(), codes, scales)
+
+
+def _table(c, b: int, dev: int, where: str, name: str):
+    if c is None:
+        return None
+    t = c.table
+    if not (_is(t, _I32, dev) and t.dim() == 2 and t.shape[0] == b):
+        _refuse(t, _I32, f"[{b}, ...]", dev, where, name)
+    return _TABLE.pack(t.data_ptr(), c.page_rows, t.shape[1], c.pool_pages)
+
+
+def _lengths(t_old, t_new, where: str) -> tuple[int, int]:
+    dev, b = t_old.get_device(), t_old.numel()
+    for t, name in ((t_old, "t_old"), (t_new, "t_new")):
+        if not (_is(t, _I64, dev) and t.shape == (b,)):
+            _refuse(t, _I64, f"[{b}]", dev, where, name)
+    return dev, b
+
+
+def _workspace(ws, nbytes: int, dev: int, where: str):
+    if ws is None:
+        return new_workspace(nbytes, dev)
+    if not (_is(ws, _U8, dev) and ws.dim() == 1):
+        _refuse(ws, _U8, "[bytes]", dev, where, "ws")
+    return ws
 
 
 def new_workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -521,48 +571,42 @@ def block_table_update(t_old: torch.Tensor, t_new: torch.Tensor, pages, free_pag
     shrink: pages (PageTable or PagedCache) gets its table rows filled in place, free_pages int32 [cap] is a stack of
     free_count (int64 [1]) page numbers.  stride 0: the table of a window cache.  Returns the new count
     (free_count_out; pass free_count itself to update it in place)."""
-    dev, b = t_old.device, int(t_old.shape[0])
     where = "block_table_update"
-    _need(t_old, torch.int64, (None,), where, "t_old", dev)
-    _need(t_new, torch.int64, (b,), where, "t_new", dev)
+    dev, b = _lengths(t_old, t_new, where)
     table = pages.table
-    _need(table, torch.int32, (b, None), where, "table", dev)
-    _need(free_pages, torch.int32, (None,), where, "free_pages", dev)
-    _need(free_count, torch.int64, (1,), where, "free_count", dev)
-    ctx, s = _on(dev, stream)
+    if not (_is(table, _I32, dev) and table.dim() == 2 and table.shape[0] == b):
+        _refuse(table, _I32, f"[{b}, ...]", dev, where, "table")
+    if not (_is(free_pages, _I32, dev) and free_pages.dim() == 1):
+        _refuse(free_pages, _I32, "[cap]", dev, where, "free_pages")
+    if not (_is(free_count, _I64, dev) and free_count.numel() == 1):
+        _refuse(free_count, _I64, "[1]", dev, where, "free_count")
+    ctx, s = _on(dev, stream, where)
     with ctx:
         if free_count_out is None:
             free_count_out = torch.empty_like(free_count)
-        _need(free_count_out, torch.int64, (1,), where, "free_count_out", dev)
-        if ws is None:
-            ws = new_workspace(16, dev)
-        _need(ws, torch.uint8, (None,), where, "ws", dev)
+        elif not (_is(free_count_out, _I64, dev) and free_count_out.numel() == 1):
+            _refuse(free_count_out, _I64, "[1]", dev, where, "free_count_out")
+        ws = _workspace(ws, 16, dev, where)
         _check(lib().dsv4kv_block_table_update(
             t_old.data_ptr(), t_new.data_ptr(), b, t_max, window, stride, lookahead, pages.page_rows, table.data_ptr(),
-            int(table.shape[1]), pages.pool_pages, free_pages.data_ptr(), int(free_pages.shape[0]),
+            table.shape[1], pages.pool_pages, free_pages.data_ptr(), free_pages.shape[0],
             free_count.data_ptr(), free_count_out.data_ptr(), ws.data_ptr(), ws.numel(), s), "dsv4kv_block_table_update")
     return free_count_out
 
 
 def new_slot_map(batch: int, capacity: int, device=None) -> SlotMap:
-    e = lambda n, dt: torch.empty(n, dtype=dt, device=device or "cuda")  # noqa: E731
+    e = lambda n, dt: torch.empty(n, dtype=dt, device="cuda" if device is None else device)  # noqa: E731
     return SlotMap(e(batch + 1, torch.int32), e(capacity, torch.int32), e(capacity, torch.int64),
                    e(capacity, torch.int32), e(capacity, torch.int32))
 
 
-def _need_slots(m: SlotMap, b: int, where: str, dev) -> int:
-    cap = int(m.seq.shape[0])
-    _need(m.cu, torch.int32, (b + 1,), where, "cu", dev)
-    for name, dt in (("seq", torch.int32), ("pos", torch.int64), ("win_slot", torch.int32), ("comp_slot", torch.int32)):
-        _need(getattr(m, name), dt, (cap,), where, name, dev)
-    return cap
-
-
-def _table_desc(p, b: int, where: str, name: str, dev):
-    if p is None:
-        return None
-    _need(p.table, torch.int32, (b, None), where, name, dev)
-    return ctypes.byref(PageTableDesc(p.table.data_ptr(), p.page_rows, int(p.table.shape[1]), p.pool_pages))
+def _need_slots(m: SlotMap, b: int, cap: int, dev: int, where: str) -> None:
+    if not (_is(m.cu, _I32, dev) and m.cu.shape == (b + 1,)):
+        _refuse(m.cu, _I32, f"[{b + 1}]", dev, where, "cu")
+    for t, dt, name in ((m.seq, _I32, "seq"), (m.pos, _I64, "pos"), (m.win_slot, _I32, "win_slot"),
+                        (m.comp_slot, _I32, "comp_slot")):
+        if not (_is(t, dt, dev) and t.shape == (cap,)):
+            _refuse(t, dt, f"[{cap}]", dev, where, name)
 
 
 def slot_map(t_old: torch.Tensor, t_new: torch.Tensor, comp, win, capacity: int, t_max: int, window: int = 128,
@@ -570,20 +614,16 @@ def slot_map(t_old: torch.Tensor, t_new: torch.Tensor, comp, win, capacity: int,
              stream=None) -> SlotMap:
     """Sequence, position and cache slots of the new tokens t_old[b] .. t_new[b] - 1 of every sequence, packed in
     order of b; comp and win are PageTables or PagedCaches (comp may be None, win too when window is 0)."""
-    dev, b = t_old.device, int(t_old.shape[0])
     where = "slot_map"
-    _need(t_old, torch.int64, (None,), where, "t_old", dev)
-    _need(t_new, torch.int64, (b,), where, "t_new", dev)
-    cd, wd = _table_desc(comp, b, where, "comp.table", dev), _table_desc(win, b, where, "win.table", dev)
-    ctx, s = _on(dev, stream)
+    dev, b = _lengths(t_old, t_new, where)
+    cd, wd = _table(comp, b, dev, where, "comp.table"), _table(win, b, dev, where, "win.table")
+    ctx, s = _on(dev, stream, where)
     with ctx:
         if out is None:
             out = new_slot_map(b, capacity, dev)
-        if _need_slots(out, b, where, dev) != capacity:
-            raise ValueError(f"{where}: out holds {int(out.seq.shape[0])} tokens, capacity is {capacity}")
-        if ws is None:
-            ws = new_workspace(16, dev)
-        _need(ws, torch.uint8, (None,), where, "ws", dev)
+        else:
+            _need_slots(out, b, capacity, dev, where)
+        ws = _workspace(ws, 16, dev, where)
         _check(lib().dsv4kv_slot_map(
             t_old.data_ptr(), t_new.data_ptr(), b, t_max, window, stride, lookahead, cd, wd, capacity,
             out.cu.data_ptr(), out.seq.data_ptr(), out.pos.data_ptr(), out.win_slot.data_ptr(),
@@ -598,28 +638,25 @@ def append_paged(s_new: torch.Tensor, w: torch.Tensor, slots: SlotMap, raw_ring:
     """Append the states s_new bf16 [capacity][512] of a slot map's tokens: raw_ring bf16 [B][window + K][512], the
     window rows and the entries that are due (w f32 [K][512]) into the paged caches, in their format.  max_new: no
     sequence has more new tokens (a tight one saves a launch)."""
-    dev, b, taps = s_new.device, int(raw_ring.shape[0]), int(w.shape[0])
     where = "append_paged"
-    cap = _need_slots(slots, b, where, dev)
-    _need(s_new, torch.bfloat16, (cap, 512), where, "s_new", dev)
-    _need(w, torch.float32, (None, 512), where, "w", dev)
-    _need(raw_ring, torch.bfloat16, (None, window + taps, 512), where, "raw_ring", dev)
-    for name, c in (("comp", comp), ("win", win)):
-        if c is not None:
-            _need(c.table, torch.int32, (b, None), where, name + ".table", dev)
-            _need_rows(c, c.pool_pages * c.page_rows, where, name, dev)
-    ctx, s = _on(dev, stream)
+    dev, b, taps, cap = s_new.get_device(), raw_ring.shape[0], w.shape[0], slots.seq.shape[0]
+    _need_slots(slots, b, cap, dev, where)
+    if not (_is(s_new, _BF, dev) and s_new.shape == (cap, 512)):
+        _refuse(s_new, _BF, f"[{cap}, 512]", dev, where, "s_new")
+    if not (_is(w, _F32, dev) and w.shape == (taps, 512)):
+        _refuse(w, _F32, "[K, 512]", dev, where, "w")
+    if not (_is(raw_ring, _BF, dev) and raw_ring.shape == (b, window + taps, 512)):
+        _refuse(raw_ring, _BF, f"[B, {window + taps}, 512]", dev, where, "raw_ring")
+    cd = _paged(comp, b, dev, where, "comp")
+    wd = None if win is None else _paged(win, b, dev, where, "win")
+    ctx, s = _on(dev, stream, where)
     with ctx:
-        if ws is None:
-            ws = new_workspace(16, dev)
-        _need(ws, torch.uint8, (None,), where, "ws", dev)
-        cd = comp.desc()
-        wd = ctypes.byref(win.desc()) if win is not None else None
+        ws = _workspace(ws, 16, dev, where)
         _check(lib().dsv4kv_append_paged(
             s_new.data_ptr(), w.data_ptr(), b, cap, slots.cu.data_ptr(), slots.seq.data_ptr(), slots.pos.data_ptr(),
             slots.win_slot.data_ptr(), slots.comp_slot.data_ptr(), taps, stride, window, lookahead,
-            cap if max_new is None else max_new, rope_dim, rope_base, raw_ring.data_ptr(), wd, ctypes.byref(cd),
-            ws.data_ptr(), ws.numel(), s), "dsv4kv_append_paged")
+            cap if max_new is None else max_new, rope_dim, rope_base, raw_ring.data_ptr(), wd, cd, ws.data_ptr(),
+            ws.numel(), s), "dsv4kv_append_paged")
 
 
 def tree_decode_paged_workspace_bytes(batch: int, heads: int, max_nodes: int, nodes: int, t_max: int, window: int = 128,
@@ -638,35 +675,39 @@ def tree_decode_paged(q: torch.Tensor, comp: PagedCache, win: PagedCache, draft:
     """Attention of drafted tokens over paged caches: q bf16 [nodes][H][512] and the rows of draft (codes
     [1][nodes][...]) packed by sequence (cu int32 [B + 1]); parent int32 [nodes] numbers within the sequence, -1 for a
     child of the last cached token.  idx int32 [nodes][k]: each node's selected entries (c4a); None: all (c128a)."""
-    n, h, d = q.shape
-    dev, b = q.device, int(t_seq.shape[0])
     where = "tree_decode_paged"
-    _need(q, torch.bfloat16, (n, h, 512), where, "q", dev)
-    _need(cu, torch.int32, (b + 1,), where, "cu", dev)
-    _need(parent, torch.int32, (n,), where, "parent", dev)
-    _need(t_seq, torch.int64, (b,), where, "t_seq", dev)
-    for name, c in (("comp", comp), ("win", win)):
-        _need(c.table, torch.int32, (b, None), where, name + ".table", dev)
-        _need_rows(c, c.pool_pages * c.page_rows, where, name, dev)
-    _need_rows(draft, n, where, "draft", dev)
-    k = 0
+    n, h, d = q.shape
+    dev, b = q.get_device(), t_seq.numel()
+    if not (_is(q, _BF, dev) and d == 512):
+        _refuse(q, _BF, "[nodes, H, 512]", dev, where, "q")
+    if not (_is(cu, _I32, dev) and cu.shape == (b + 1,)):
+        _refuse(cu, _I32, f"[{b + 1}]", dev, where, "cu")
+    if not (_is(parent, _I32, dev) and parent.shape == (n,)):
+        _refuse(parent, _I32, f"[{n}]", dev, where, "parent")
+    if not (_is(t_seq, _I64, dev) and t_seq.dim() == 1):
+        _refuse(t_seq, _I64, "[B]", dev, where, "t_seq")
+    cd, wd = _paged(comp, b, dev, where, "comp"), _paged(win, b, dev, where, "win")
+    dd = _CACHE.pack(draft.fmt, draft.dim, n, *_rows(draft, n, dev, where, "draft"))
+    k, ip = 0, None
     if idx is not None:
-        _need(idx, torch.int32, (n, None), where, "idx", dev)
-        k = int(idx.shape[1])
+        if not (_is(idx, _I32, dev) and idx.dim() == 2 and idx.shape[0] == n):
+            _refuse(idx, _I32, f"[{n}, k]", dev, where, "idx")
+        k, ip = idx.shape[1], idx.data_ptr()
     if sm_scale is None:
         sm_scale = d ** -0.5
-    ctx, s = _on(dev, stream)
+    ctx, s = _on(dev, stream, where)
     with ctx:
+        dt = _F32 if out_fp32 else _BF
         if out is None:
-            out = torch.empty((n, h, d), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=dev)
-        _need(out, torch.float32 if out_fp32 else torch.bfloat16, (n, h, 512), where, "out", dev)
+            out = torch.empty((n, h, d), dtype=dt, device=q.device)
+        elif not (_is(out, dt, dev) and out.shape == q.shape):
+            _refuse(out, dt, f"[{n}, {h}, 512]", dev, where, "out")
         if ws is None:
-            ws = new_workspace(tree_decode_paged_workspace_bytes(b, h, max_nodes, n, t_max, window, stride, k), dev)
-        _need(ws, torch.uint8, (None,), where, "ws", dev)
-        cd, wd = comp.desc(), win.desc()
-        dd = CacheDesc(draft.fmt, draft.dim, n, _ptr(draft.codes), _ptr(draft.scales))
+            ws = new_workspace(tree_decode_paged_workspace_bytes(b, h, max_nodes, n, t_max, window, stride, k), q.device)
+        else:
+            ws = _workspace(ws, 0, dev, where)
         _check(lib().dsv4kv_tree_decode_paged(
-            q.data_ptr(), ctypes.byref(cd), ctypes.byref(wd), ctypes.byref(dd), cu.data_ptr(), parent.data_ptr(),
-            _ptr(idx), b, h, n, max_nodes, t_seq.data_ptr(), t_max, window, stride, k, sm_scale, rope_dim, rope_base,
-            int(out_fp32), out.data_ptr(), ws.data_ptr(), ws.numel(), s), "dsv4kv_tree_decode_paged")
+            q.data_ptr(), cd, wd, dd, cu.data_ptr(), parent.data_ptr(), ip, b, h, n, max_nodes, t_seq.data_ptr(), t_max,
+            window, stride, k, sm_scale, rope_dim, rope_base, out_fp32, out.data_ptr(), ws.data_ptr(), ws.numel(), s),
+            "dsv4kv_tree_decode_paged")
     return out

@@ -130,8 +130,8 @@ struct Seg {  // the part of a group that a pair works on
   int n, full;              // compressed rows listed (the most any node may see), whole tiles that every node sees
 };
 
-// Who sees a row: the positions [lo, hi]; lo < 0: drafted node -1 - lo, its descendants.
-struct Key {
+// Who sees a row: the positions [lo, hi]; a drafted row of the dense form: nobody by its key, but the node's descendants.
+struct __align__(8) Key {
   int lo, hi;
 };
 constexpr int kNever = 0x7fffffff;
@@ -148,7 +148,7 @@ struct __align__(16) Ctl {
   int node_pos;   // (selected form) the node's position
   int b, g, t0;   // (equal runs) where this pair's run starts
   int whole, share, units;
-  Key key[2][kRows];              // the rows of a tile that the loader warps brought
+  __align__(16) Key key[2][kRows];  // the rows of a tile that the loader warps brought
   uint32_t plain[2][4];           // all of a value warp's rows are there and every query sees them
   __align__(16) float scale[2][kRows];
   __align__(16) float lscale[2][kRows];  // log2 of the scale
@@ -257,16 +257,12 @@ __device__ __forceinline__ int tiles_of(const Params& p, int n, int w, int m) {
   return ((p.idx ? min(n, p.k) : n) + w + m + kRows - 1) / kRows;
 }
 
-// Pool row of logical row i; -1 (flagged) when its page is outside the pool or the table has no entry for it.
-__device__ __forceinline__ int64_t map_row(const Rows& r, int b, int i, uint32_t* status) {
+// Pool row of logical row i; -1 when its page is outside the pool or the table has no entry for it.
+__device__ __forceinline__ int64_t map_row(const Rows& r, int b, int i) {
   if (!r.table) return i;
   const int pi = i / r.page;
   const int32_t pg = pi < r.tstride ? __ldg(r.table + size_t(b) * r.tstride + pi) : -1;
-  if (pg < 0 || pg >= r.pages) {
-    set_status(status, DSV4KV_DEV_BAD_PAGE);
-    return -1;
-  }
-  return int64_t(pg) * r.page + (i - pi * r.page);
+  return pg >= 0 && pg < r.pages ? int64_t(pg) * r.page + (i - pi * r.page) : -1;
 }
 
 // Pool rows of the two 64-row halves of whole tile T (pages hold whole halves); false: a bad page.
@@ -283,48 +279,47 @@ __device__ __forceinline__ bool tma_rows(const Params& p, int b, int T, int32_t 
 }
 
 // Row r of tile T: its cache and pool row (null: there is none, or no query of the group sees it) and who sees it.
-// Whole tiles (T < s.full) need nothing of the tree.
+// Whole tiles (T < s.full) need nothing of the tree; for the others `met` waits for it (warp-uniform), after the index
+// and table reads are on their way.  Pages are flagged only for rows that are needed.
+template <class Met>
 __device__ __forceinline__ const Rows* row_source(const Params& p, const Seg& s, const Ctl* ctl, int T, int r,
-                                                  int64_t* row, Key* key) {
+                                                  int64_t* row, Key* key, Met met) {
   const int u = kRows * T + r, j = u - s.n;
-  const Rows* src = nullptr;
-  int i = -1;
+  const Rows* src = j < 0 ? &p.comp : j < s.w ? &p.win : j - s.w < s.m ? &p.draft : nullptr;
+  int i = j < 0 ? u : j < s.w ? j : s.c0 + (j - s.w);
+  if (j < 0 && p.idx) i = __ldg(p.idx + size_t(s.c0 + s.g) * p.k + u);
+  *row = src && i >= 0 && (j >= 0 || i < entries(s.t + s.m - 1, p.window, p.stride)) ? map_row(*src, s.b, i) : -1;
   *key = Key{0, kNever};
-  if (j < 0) {  // compressed
-    src = &p.comp;
-    i = u;
-    if (p.idx) {
-      const int n = entries(ctl->node_pos, p.window, p.stride);
-      i = u < min(p.k, n) ? __ldg(p.idx + size_t(s.c0 + s.g) * p.k + u) : -1;
-      if (i >= n) {
-        set_status(p.status, DSV4KV_DEV_BAD_INDEX);
-        i = -1;
+  bool need = src && i >= 0;
+  if (T >= s.full) {
+    if (!met()) need = false;
+    if (j < 0) {
+      if (p.idx) {
+        const int n = entries(ctl->node_pos, p.window, p.stride);
+        if (u >= min(p.k, n)) need = false;
+        if (need && i >= n) {
+          set_status(p.status, DSV4KV_DEV_BAD_INDEX);
+          need = false;
+        }
+      } else {
+        key->lo = p.window + p.stride * (u + 1);  // N(p) > u
+        if (key->lo > ctl->p_max) need = false;
       }
-    } else if (T >= s.full) {
-      key->lo = p.window + p.stride * (u + 1);  // N(p) > u
-      if (key->lo > ctl->p_max) i = -1;
+    } else if (j < s.w) {  // window row j holds the last position congruent to j
+      key->hi = s.t - 1 - (s.t - 1 - j) % p.window + p.window;
+      if (p.idx) {
+        if (key->hi < ctl->node_pos) need = false;
+        key->hi = kNever;
+      }
+    } else if (j - s.w < s.m) {
+      if (!p.idx) *key = Key{kNever, 0};  // (see the ancestor bits)
+      else if (!((ctl->anc[0][(j - s.w) >> 5] >> ((j - s.w) & 31)) & 1u)) need = false;
     }
-  } else if (j < s.w) {  // window row j holds the last position congruent to j
-    src = &p.win;
-    i = j;
-    key->hi = s.t - 1 - (s.t - 1 - j) % p.window + p.window;
-    if (p.idx) {
-      if (key->hi < ctl->node_pos) i = -1;
-      key->hi = kNever;
-    }
-  } else if (j - s.w < s.m) {
-    src = &p.draft;
-    i = j - s.w;
-    if (!p.idx) key->lo = -1 - i;
-    else if (!((ctl->anc[0][i >> 5] >> (i & 31)) & 1u)) i = -1;
-    if (i >= 0) i += s.c0;
   }
-  *row = i >= 0 ? map_row(*src, s.b, i, p.status) : -1;
-  if (*row < 0) {
-    key->lo = kNever;
-    src = nullptr;
-  }
-  return src;
+  if (need && *row < 0) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+  if (need && *row >= 0) return src;
+  key->lo = kNever;
+  return nullptr;
 }
 
 // ---------------------------------------------------------------- loader warps
@@ -350,8 +345,7 @@ __host__ __device__ constexpr int row_bytes(int fmt) {
 // weights).  A batch is 8 units a lane: fetch() issues its loads, put() converts it.
 template <int FMT, int kR>
 struct Dequant {
-  static constexpr bool kFp4 = FMT == DSV4KV_FP4_E2M1_G16;
-  [[maybe_unused]] static constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16;
+  static constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16, kFp4 = FMT == DSV4KV_FP4_E2M1_G16;
   static constexpr int kN = 8;
   uint4 raw[kN];
   uint32_t sc[kFp4 ? kN : 1];
@@ -770,12 +764,21 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           for (int x = 0; x < C::kValWarps; ++x) pl &= ctl->plain[sb][x];
           plain = pl == kFull;
           if (!plain && live) {
+            // compressed and window rows by position, drafted ones (consecutive) by the node's ancestor bits
             seen = 0;
-#pragma unroll 4
-            for (int x = 0; x < kCols; ++x) {
-              const Key k = ctl->key[sb][r0 + x];
-              const bool v = k.lo >= 0 ? pos >= k.lo && pos <= k.hi : (anc[(-1 - k.lo) >> 5] >> ((-1 - k.lo) & 31)) & 1u;
-              if (v) seen |= 1u << x;
+            const int4* keys = reinterpret_cast<const int4*>(&ctl->key[sb][r0]);
+#pragma unroll
+            for (int x = 0; x < kCols; x += 2) {
+              const int4 k = keys[x / 2];
+              seen |= (pos >= k.x && pos <= k.y ? 1u : 0u) << x;
+              seen |= (pos >= k.z && pos <= k.w ? 2u : 0u) << x;
+            }
+            const int d0 = kRows * T + r0 - s.n - s.w;  // the first row as a drafted node
+            if (!p.idx && d0 > -kCols && d0 < s.m) {
+              const int w = max(d0, 0) >> 5;
+              uint32_t bits = __funnelshift_r(anc[w], w + 1 < kMaxNodes / 32 ? anc[w + 1] : 0u, max(d0, 0) & 31);
+              if (d0 < 0) bits <<= -d0;
+              seen |= kCols == 32 ? bits : bits & ((1u << (kCols & 31)) - 1u);
             }
           }
         }
@@ -977,22 +980,24 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       float sr[kX];
       Key key[kX];
     };
-    int met = -1;  // the last part whose nodes were waited for
+    int last_met = -1;  // the last part whose nodes were waited for
     bool ok = true;
+    auto met = [&]() {
+      if (last_met != segs) {
+        ok = warp_wait(&ctl->meta, segs & 1, abort, lane);
+        last_met = segs;
+      }
+      return ok;
+    };
     auto resolve = [&](Set& e, int T) {
       int32_t trow[2];
       e.tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
       e.row0 = half ? trow[1] : trow[0];
       if (e.tma) return;
-      if (T >= s.full && met != segs) {
-        ok = warp_wait(&ctl->meta, segs & 1, abort, lane);
-        met = segs;
-        if (!ok) return;
-      }
 #pragma unroll
       for (int x = 0; x < kX; ++x) {
         int64_t row;
-        const Rows* src = row_source(p, s, ctl, T, C::kValRows * vw + 32 * x + lane, &row, &e.key[x]);
+        const Rows* src = row_source(p, s, ctl, T, C::kValRows * vw + 32 * x + lane, &row, &e.key[x], met);
         e.my[x] = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
         if (FMT == DSV4KV_FP4_E2M1_G16)
           e.mysc[x] = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
@@ -1003,7 +1008,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       load_part();
       const int nt = s.t1 - s.t0;
       Set cur, nxt;
-      Dequant<FMT, 32> dq;
+      Dequant<C::kQuant ? FMT : DSV4KV_FP8_E4M3_ROW, 32> dq;
       resolve(cur, s.t0);
       if (!ok) break;
       if constexpr (C::kQuant) dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, 0, lane);
@@ -1039,9 +1044,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         const uint32_t bar = lead_addr(&ctl->v_full[half]);
         if (cur.tma) {
           if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[half], 2 * kVPart);
+            const bool mine = vw % (C::kValWarps / 2) == 0;  // one warp a half
+            if (mine && rank == 0) mbar_arrive_expect_tx(&ctl->v_full[half], 2 * kVPart);
             else mbar_arrive_pair(bar);
-            tma_load_3d_pair(sV + half * kVPart, &tm_comp, bar, 0, cur.row0, 4 * rank);
+            if (mine) tma_load_3d_pair(sV + half * kVPart, &tm_comp, bar, 0, cur.row0, 4 * rank);
             mbar_arrive(&ctl->v_here[half]);  // (nobody waits for a whole tile's)
           }
           __syncwarp();
@@ -1088,21 +1094,23 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       const uint8_t *my, *mysc;
       float inv;
     };
-    int met = -1;
+    int last_met = -1;
     bool ok = true;
+    auto met = [&]() {
+      if (last_met != segs) {
+        ok = warp_wait(&ctl->meta, segs & 1, abort, lane);
+        last_met = segs;
+      }
+      return ok;
+    };
     auto resolve = [&](Set& e, int T) {
       int32_t trow[2];
       e.tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
       e.row0 = rank ? trow[1] : trow[0];
       if (e.tma) return;
-      if (T >= s.full && met != segs) {
-        ok = warp_wait(&ctl->meta, segs & 1, abort, lane);
-        met = segs;
-        if (!ok) return;
-      }
       int64_t row;
       Key key;
-      const Rows* src = row_source(p, s, ctl, T, kKeys * rank + 16 * kw + (lane & 15), &row, &key);
+      const Rows* src = row_source(p, s, ctl, T, kKeys * rank + 16 * kw + (lane & 15), &row, &key, met);
       e.my = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
       if (FMT == DSV4KV_FP4_E2M1_G16)
         e.mysc = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
@@ -1115,7 +1123,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       load_part();
       const int nt = s.t1 - s.t0;
       Set cur, nxt;
-      Dequant<FMT, 16> dq;
+      Dequant<C::kQuant ? FMT : DSV4KV_FP8_E4M3_ROW, 16> dq;
       resolve(cur, s.t0);
       if (!ok) break;
       if constexpr (C::kQuant) dq.fetch(cur.my, cur.mysc, 0, 0, lane);
@@ -1353,7 +1361,11 @@ dsv4kv_status tree_decode_launch(const TreeArgs& a, void* ws, cudaStream_t strea
   if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "tree_kernel: %s", cudaGetErrorString(e));
   dsv4kv_status st = check_launch("tree_kernel");
   if (st != DSV4KV_OK) return st;
-  if (P > 1) launch_pdl(tree_combine, dim3(unsigned(16 * P)), dim3(256), 0, stream, p, P);
+  // (a call whose groups fit the pairs and have few tiles never cuts one: see the split rule)
+  const int k = a.idx ? a.k : 0;
+  const bool never = groups_max(a.batch, a.heads, a.nodes, k) <= P &&
+                     tiles_max(a.max_nodes, a.t_max, a.window, a.stride, k) <= kSplitCost + 1;
+  if (P > 1 && !never) launch_pdl(tree_combine, dim3(unsigned(16 * P)), dim3(256), 0, stream, p, P);
   return check_launch("tree_combine");
 }
 
