@@ -286,8 +286,25 @@ struct AppendParams {
 };
 
 struct Tok {
-  int i, b, pos, first;  // token, sequence, position, the sequence's first new token
+  int i, b, pos, first, slot;  // token, sequence, position, the sequence's first new token, its entry's pool row
 };
+
+// While rows are loaded and summed a lane holds channels [8 lane, 8 lane + 8) and [256 + 8 lane, ..), so that every load
+// of a row is one contiguous 512-byte piece; rotation and storing want channels [16 lane, 16 lane + 16).
+__device__ __forceinline__ void to_consecutive(float (&x)[kPer], int lane) {
+  const int from = (2 * lane) & 31;  // the lane that holds 8-channel pieces 2 lane (2 lane + 1: the next one)
+  const bool upper = lane >= 16;     // of the upper 256 channels
+  float y[kPer];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a0 = __shfl_sync(kFull, x[e], from), a1 = __shfl_sync(kFull, x[8 + e], from);
+    const float b0 = __shfl_sync(kFull, x[e], from + 1), b1 = __shfl_sync(kFull, x[8 + e], from + 1);
+    y[e] = upper ? a1 : a0;
+    y[8 + e] = upper ? b1 : b0;
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = y[e];
+}
 
 // x = channels [16 lane, 16 lane + 16) of a row, its rotary pairs rotated at pos.
 // theta: pair `lane`'s theta / pi (where there are at most 32 pairs).
@@ -343,27 +360,21 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* x) {
   x[6] = bf16lo(v.w); x[7] = bf16hi(v.w);
 }
 
-// The state row of position q of token k's sequence (this lane's channels): a new token's or the raw ring's.
+// The state row of position q of token k's sequence: a new token's or the raw ring's (this lane's first piece).
 __device__ __forceinline__ const uint16_t* state_row(const AppendParams& p, const Tok& k, int q, int lane) {
   const int i = k.i - (k.pos - q);
-  if (i >= k.first) return p.s_new + size_t(i) * kD + kPer * lane;
+  if (i >= k.first) return p.s_new + size_t(i) * kD + 8 * lane;
   const int R = p.window + p.k_taps;
-  return p.ring + (size_t(k.b) * R + q % R) * kD + kPer * lane;
+  return p.ring + (size_t(k.b) * R + q % R) * kD + 8 * lane;
 }
+__device__ __forceinline__ uint4 first_piece(const uint16_t* row) { return *reinterpret_cast<const uint4*>(row); }
+__device__ __forceinline__ uint4 second_piece(const uint16_t* row) { return *reinterpret_cast<const uint4*>(row + 256); }
 
-__device__ __forceinline__ void add_tap(float (&acc)[kPer], const float (&w)[kPer], const uint4& a, const uint4& b) {
-  float x[kPer];
-  unpack8(a, x);
-  unpack8(b, x + 8);
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w[e], x[e], acc[e]);
-}
-__device__ __forceinline__ void load_weights(float (&w)[kPer], const float* src) {
-#pragma unroll
-  for (int q = 0; q < kPer / 4; ++q) {
-    const float4 v = *reinterpret_cast<const float4*>(src + 4 * q);
-    w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
-  }
+__device__ __forceinline__ void add8(float* acc, const float4& w0, const float4& w1, const uint4& v) {
+  acc[0] = fmaf(w0.x, bf16lo(v.x), acc[0]); acc[1] = fmaf(w0.y, bf16hi(v.x), acc[1]);
+  acc[2] = fmaf(w0.z, bf16lo(v.y), acc[2]); acc[3] = fmaf(w0.w, bf16hi(v.y), acc[3]);
+  acc[4] = fmaf(w1.x, bf16lo(v.z), acc[4]); acc[5] = fmaf(w1.y, bf16hi(v.z), acc[5]);
+  acc[6] = fmaf(w1.z, bf16lo(v.w), acc[6]); acc[7] = fmaf(w1.w, bf16hi(v.w), acc[7]);
 }
 
 // Appends i to list[n ..] where `keep`, in thread order; returns the new length.  All threads call it.
@@ -383,22 +394,23 @@ __device__ __forceinline__ int push_ordered(bool keep, int i, int32_t* list, int
   return all;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kAppThreads)
+template <int FMT, bool kLong>
+__global__ void __launch_bounds__(kAppThreads, 2)
     append_paged_kernel(const __grid_constant__ AppendParams p) {
   __shared__ int32_t rows[kMaxTokens], ents[kMaxTokens];
   __shared__ int wcnt[kAppWarps];
-  extern __shared__ __align__(16) float red[];  // long entries: [warp][group][512]
+  extern __shared__ __align__(16) float red[];  // long entries: [warp][group][512]; short ones: the weights
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i_first = blockIdx.x * p.per, i_end = min(p.tokens, i_first + p.per);
   const int R = p.window + p.k_taps;
   const double theta = p.rope.theta_pi[lane];
   pdl_trigger();
   pdl_wait();
-  // a token of the list: its sequence and the sequence's first new token
+  // a token of a list
   auto token = [&](int i) {
-    const int b = p.seq[i];
-    return Tok{i, b, int(p.pos[i]), p.cu[b]};
+    const int b = __ldg(p.seq + i);
+    const int pos = int(__ldg(p.pos + i)), slot = __ldg(p.comp_slot + i);
+    return Tok{i, b, pos, __ldg(p.cu + b), slot};
   };
   int n_rows = 0, n_ents = 0;
   for (int i0 = i_first; i0 < i_end; i0 += kAppThreads) {
@@ -431,42 +443,70 @@ __global__ void __launch_bounds__(kAppThreads)
   // ring and window rows
   for (int r = warp; r < n_rows; r += kAppWarps) {
     const Tok k = token(rows[r]);
-    const uint4* src = reinterpret_cast<const uint4*>(p.s_new + size_t(k.i) * kD + kPer * lane);
-    const uint4 v0 = src[0], v1 = src[1];
+    const uint16_t* src = p.s_new + size_t(k.i) * kD + 8 * lane;
+    const uint4 v0 = first_piece(src), v1 = second_piece(src);
     if ((p.parts & kPartRing) && p.cu[k.b + 1] - 1 - k.i < R) {
-      uint4* dst = reinterpret_cast<uint4*>(p.ring + (size_t(k.b) * R + k.pos % R) * kD + kPer * lane);
-      dst[0] = v0;
-      dst[1] = v1;
+      uint16_t* dst = p.ring + (size_t(k.b) * R + k.pos % R) * kD + 8 * lane;
+      *reinterpret_cast<uint4*>(dst) = v0;
+      *reinterpret_cast<uint4*>(dst + 256) = v1;
     }
     const int slot = p.win_slot[k.i];
     if ((p.parts & kPartWindow) && slot >= 0 && slot < p.win_rows) {
       float x[kPer];
       unpack8(v0, x);
       unpack8(v1, x + 8);
+      to_consecutive(x, lane);
       rotate_row(x, p, theta, k.pos, lane);
       store_row<FMT>(x, lane, slot, p.win_codes, p.win_scales);
     }
   }
-  if (p.k_taps <= kLongTaps) {
-    for (int r = warp; r < n_ents; r += kAppWarps) {
-      const Tok k = token(ents[r]);
+  if constexpr (!kLong) {
+    if (n_ents == 0) return;
+    // weights [tap][quarter][lane] float4: a lane's two pieces of 8 channels in four conflict-free reads
+    float4* sw = reinterpret_cast<float4*>(red);
+    for (int i = threadIdx.x; i < p.k_taps * (kD / 4); i += kAppThreads) {
+      const int j = i / (kD / 4), c = i % (kD / 4);  // quad c: lane (c / 2) % 32, quarter 2 (c / 64) + c % 2
+      sw[(j * 4 + 2 * (c >> 6) + (c & 1)) * 32 + ((c >> 1) & 31)] = reinterpret_cast<const float4*>(p.w)[i];
+    }
+    __syncthreads();
+    // consecutive entries to one warp: the rows that two entries share come from L1 the second time
+    const int per = (n_ents + kAppWarps - 1) / kAppWarps, end = min(n_ents, (warp + 1) * per);
+    Tok next = warp * per < end ? token(ents[warp * per]) : Tok{};
+#pragma unroll 1
+    for (int r = warp * per; r < end; ++r) {
+      const Tok k = next;
+      if (r + 1 < end) next = token(ents[r + 1]);
       const int q0 = k.pos + 1 + p.lookahead - p.window - p.k_taps;
       float acc[kPer];
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-      for (int j = max(0, -q0); j < p.k_taps; ++j) {
-        const uint4* src = reinterpret_cast<const uint4*>(state_row(p, k, q0 + j, lane));
-        float w[kPer];
-        load_weights(w, p.w + size_t(j) * kD + kPer * lane);
-        add_tap(acc, w, src[0], src[1]);
+#pragma unroll 2
+      for (int j0 = max(0, -q0); j0 < p.k_taps; j0 += 4) {
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          a[x] = b[x] = make_uint4(0, 0, 0, 0);
+          if (j0 + x < p.k_taps) {
+            const uint16_t* src = state_row(p, k, q0 + j0 + x, lane);
+            a[x] = first_piece(src);
+            b[x] = second_piece(src);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (j0 + x >= p.k_taps) break;
+          const float4* w = sw + (j0 + x) * 128 + lane;
+          add8(acc, w[0], w[32], a[x]);
+          add8(acc + 8, w[64], w[96], b[x]);
+        }
       }
+      to_consecutive(acc, lane);
       rotate_row(acc, p, theta, q0 + p.k_taps - p.stride, lane);
-      store_row<FMT>(acc, lane, p.comp_slot[k.i], p.comp_codes, p.comp_scales);
+      store_row<FMT>(acc, lane, k.slot, p.comp_codes, p.comp_scales);
     }
     return;
   }
-  for (int r0 = 0; r0 < n_ents; r0 += kGroup) {
+  if constexpr (kLong) for (int r0 = 0; r0 < n_ents; r0 += kGroup) {
     Tok k[kGroup];
     int q0[kGroup];
     float acc[kGroup][kPer];
@@ -478,22 +518,26 @@ __global__ void __launch_bounds__(kAppThreads)
       for (int e = 0; e < kPer; ++e) acc[g][e] = 0.f;
     }
     const int ng = min(kGroup, n_ents - r0);
-#pragma unroll 2
+#pragma unroll 1
     for (int j = warp; j < p.k_taps; j += kAppWarps) {
-      float w[kPer];
       uint4 a[kGroup], b[kGroup];
 #pragma unroll
       for (int g = 0; g < kGroup; ++g) {
         a[g] = b[g] = make_uint4(0, 0, 0, 0);
         if (g < ng && q0[g] + j >= 0) {
-          const uint4* src = reinterpret_cast<const uint4*>(state_row(p, k[g], q0[g] + j, lane));
-          a[g] = src[0];
-          b[g] = src[1];
+          const uint16_t* src = state_row(p, k[g], q0[g] + j, lane);
+          a[g] = first_piece(src);
+          b[g] = second_piece(src);
         }
       }
-      load_weights(w, p.w + size_t(j) * kD + kPer * lane);
+      const float4* wr = reinterpret_cast<const float4*>(p.w + size_t(j) * kD + 8 * lane);
+      float4 w0 = __ldg(wr), w1 = __ldg(wr + 1);
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) add_tap(acc[g], w, a[g], b[g]);
+      for (int g = 0; g < kGroup; ++g) add8(acc[g], w0, w1, a[g]);
+      w0 = __ldg(wr + 64);
+      w1 = __ldg(wr + 65);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) add8(acc[g] + 8, w0, w1, b[g]);
     }
     if (r0) __syncthreads();  // the previous group's sums are read
 #pragma unroll
@@ -501,7 +545,7 @@ __global__ void __launch_bounds__(kAppThreads)
       if (g >= ng) break;
       float4* dst = reinterpret_cast<float4*>(red + (size_t(warp) * kGroup + g) * kD) + lane;
 #pragma unroll
-      for (int q = 0; q < kPer / 4; ++q)  // (element 16 lane + 4 q at [q][lane]: conflict-free)
+      for (int q = 0; q < kPer / 4; ++q)  // (conflict-free: quarter q of every lane side by side)
         dst[32 * q] = make_float4(acc[g][4 * q], acc[g][4 * q + 1], acc[g][4 * q + 2], acc[g][4 * q + 3]);
     }
     __syncthreads();
@@ -509,6 +553,7 @@ __global__ void __launch_bounds__(kAppThreads)
       float x[kPer];
 #pragma unroll
       for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+#pragma unroll 1
       for (int ww = 0; ww < kAppWarps; ++ww) {
         const float4* src = reinterpret_cast<const float4*>(red + (size_t(ww) * kGroup + warp) * kD) + lane;
 #pragma unroll
@@ -517,24 +562,32 @@ __global__ void __launch_bounds__(kAppThreads)
           x[4 * q] += v.x; x[4 * q + 1] += v.y; x[4 * q + 2] += v.z; x[4 * q + 3] += v.w;
         }
       }
+      to_consecutive(x, lane);
       const Tok t = token(ents[r0 + warp]);
       rotate_row(x, p, theta, t.pos + 1 + p.lookahead - p.window - p.stride, lane);
-      store_row<FMT>(x, lane, p.comp_slot[t.i], p.comp_codes, p.comp_scales);
+      store_row<FMT>(x, lane, t.slot, p.comp_codes, p.comp_scales);
     }
   }
 }
 
-template <int FMT>
-cudaError_t launch_append(const AppendParams& p, size_t smem, cudaStream_t stream) {
+template <int FMT, bool kLong>
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
+  const size_t most = kLong ? kAppWarps * kGroup * kD * sizeof(float) : kLongTaps * kD * sizeof(float);
   if (!done_on_device(ready)) {
-    const cudaError_t e = cudaFuncSetAttribute(append_paged_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(kAppWarps * kGroup * kD * sizeof(float)));
+    const cudaError_t e =
+        cudaFuncSetAttribute(append_paged_kernel<FMT, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
     if (e != cudaSuccess) return e;
     mark_done_on_device(ready);
   }
   const dim3 grid(unsigned((p.tokens + p.per - 1) / p.per));
-  return launch_pdl(append_paged_kernel<FMT>, grid, dim3(kAppThreads), smem, stream, p);
+  const bool entries = p.parts & kPartEntries;
+  const size_t smem = !entries ? 0 : kLong ? most : size_t(p.k_taps) * kD * sizeof(float);
+  return launch_pdl(append_paged_kernel<FMT, kLong>, grid, dim3(kAppThreads), smem, stream, p);
+}
+template <int FMT>
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+  return p.k_taps > kLongTaps ? launch_append<FMT, true>(p, stream) : launch_append<FMT, false>(p, stream);
 }
 
 }  // namespace
@@ -553,7 +606,7 @@ dsv4kv_status block_table_update_launch(const int64_t* t_old, const int64_t* t_n
                       pool_pages, free_pages, free_cap, free_count, free_count_out, static_cast<uint32_t*>(ws)};
   // a decode step changes at most a page or so per sequence; prompts bring up to table_stride of them
   const int64_t most = int64_t(batch) * table_stride;
-  const int grid = int(std::max<int64_t>(1, std::min<int64_t>(sm_count(), most / (16 * kTabThreads))));
+  const int grid = int(std::max<int64_t>(1, std::min<int64_t>(64, most / (2 * kTabThreads))));
   launch_pdl(block_table_kernel, dim3(grid), dim3(kTabThreads), size_t(2 * (batch + 1)) * sizeof(int32_t), stream, p);
   return check_launch("block_table_kernel");
 }
@@ -600,20 +653,22 @@ dsv4kv_status append_paged_launch(const void* s_new, const float* w, int batch, 
   p.comp_rows = comp.rows;
   p.status = static_cast<uint32_t*>(ws);
   rope_table_fill(&p.rope, rope_dim, rope_base);
+  // Few tokens: spread over the SMs.  Many: long entries (128 tokens apart in c128a) two CTAs an SM, so that up to four
+  // share a weight read; short ones in runs of at most 128 tokens; the rows of a second pass 32 tokens a CTA (they
+  // are the last ones of every sequence).
   const bool lng = k_taps > kLongTaps;
-  // few tokens: spread them over the SMs; many: enough a CTA that four long entries share their weights
-  const int64_t spread = (int64_t(tokens) + 4 * sm_count() - 1) / (4 * sm_count());
-  p.per = int(std::max<int64_t>(1, std::min<int64_t>(spread, lng ? kMaxTokens : 128)));
-  const size_t smem = lng ? kAppWarps * kGroup * kD * sizeof(float) : 0;
+  const int64_t ctas = int64_t(lng ? 2 : 4) * sm_count();
   const bool two = max_new > int64_t(lookahead) + 1;
   for (int pass = 0; pass < (two ? 2 : 1); ++pass) {
-    p.parts = !two ? kPartEntries | kPartWindow | kPartRing : pass == 0 ? kPartEntries | kPartWindow : kPartRing;
+    p.parts = !two ? kPartEntries | kPartWindow | kPartRing : pass == 0 ? kPartEntries : kPartWindow | kPartRing;
+    p.per = int(std::max<int64_t>(1, std::min<int64_t>((int64_t(tokens) + ctas - 1) / ctas,
+                                                       pass == 1 ? 32 : lng ? kMaxTokens : 128)));
     cudaError_t e;
     switch (comp.fmt) {
-      case DSV4KV_BF16: e = launch_append<DSV4KV_BF16>(p, smem, stream); break;
-      case DSV4KV_FP8_E4M3_ROW: e = launch_append<DSV4KV_FP8_E4M3_ROW>(p, smem, stream); break;
-      case DSV4KV_FP4_E2M1_G16: e = launch_append<DSV4KV_FP4_E2M1_G16>(p, smem, stream); break;
-      default: e = launch_append<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(p, smem, stream); break;
+      case DSV4KV_BF16: e = launch_append<DSV4KV_BF16>(p, stream); break;
+      case DSV4KV_FP8_E4M3_ROW: e = launch_append<DSV4KV_FP8_E4M3_ROW>(p, stream); break;
+      case DSV4KV_FP4_E2M1_G16: e = launch_append<DSV4KV_FP4_E2M1_G16>(p, stream); break;
+      default: e = launch_append<DSV4KV_FP8_E4M3_ROW_ROPE_BF16>(p, stream); break;
     }
     if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "append_paged_kernel: %s", cudaGetErrorString(e));
     const dsv4kv_status st = check_launch("append_paged_kernel");
