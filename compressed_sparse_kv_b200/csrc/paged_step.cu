@@ -28,8 +28,8 @@
 // latency for a decode step.  Entries read rows of the raw ring that tokens of the
 // same call replace when a sequence has more than lookahead + 1 new ones
 // (entry taps reach back to p + 1 + lookahead - (window + k_taps), the row
-// replaced by token p' is p' - (window + k_taps)); the ring is then written by
-// a second launch.
+// replaced by token p' is p' - (window + k_taps)); the ring
+// (and the window, whose rows are the last ones too) is then written by a second launch, one warp a row.
 #include <cmath>
 #include <cstdint>
 
@@ -192,13 +192,16 @@ __device__ __forceinline__ int32_t slot_of(const PageDesc& d, int b, int row, ui
 }
 
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams p) {
-  extern __shared__ int32_t pre[];  // first token of every sequence, clamped to the capacity
+  extern __shared__ int32_t pre[];  // first token of every sequence, clamped to the capacity; its old and new length
+  int32_t *old_len = pre + p.batch + 1, *new_len = old_len + p.batch;
   pdl_trigger();
   pdl_wait();
   const uint64_t sum = block_prefix<kSlotThreads>(
       p.batch,
       [&](int b) -> uint64_t {
         const int64_t o = clamp_len(p.t_old[b], p.t_max, p.status), n = clamp_len(p.t_new[b], p.t_max, p.status);
+        old_len[b] = int32_t(o);
+        new_len[b] = int32_t(n);
         return uint64_t(max(int64_t(0), n - o));
       },
       [&](int b, uint64_t v) {
@@ -228,8 +231,8 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
       if (i >= total) continue;
       while (pre[b + 1] <= i) ++b;  // (ends: i < pre[batch])
       if (of != b) {
-        o = int(clamp_len(p.t_old[b], p.t_max, nullptr));
-        n = int(clamp_len(p.t_new[b], p.t_max, nullptr));
+        o = old_len[b];
+        n = new_len[b];
         of = b;
       }
       const int pp = o + (i - pre[b]);
@@ -263,7 +266,8 @@ constexpr int kAppWarps = 8;
 constexpr int kAppThreads = 32 * kAppWarps;
 constexpr int kD = 512, kPer = kD / 32;
 constexpr int kMaxTokens = 512;  // tokens a CTA
-constexpr int kGroup = 4;        // long entries summed together
+constexpr int kGroup = 2;        // long entries summed together
+constexpr int kAhead = 4;        // taps of them that a warp has in flight
 constexpr int kLongTaps = 32;    // entries of more taps are summed by the whole CTA
 
 enum : int { kPartEntries = 1, kPartWindow = 2, kPartRing = 4 };
@@ -507,6 +511,7 @@ __global__ void __launch_bounds__(kAppThreads, 2)
     return;
   }
   if constexpr (kLong) for (int r0 = 0; r0 < n_ents; r0 += kGroup) {
+    const int ng = min(kGroup, n_ents - r0);
     Tok k[kGroup];
     int q0[kGroup];
     float acc[kGroup][kPer];
@@ -517,27 +522,32 @@ __global__ void __launch_bounds__(kAppThreads, 2)
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[g][e] = 0.f;
     }
-    const int ng = min(kGroup, n_ents - r0);
 #pragma unroll 1
-    for (int j = warp; j < p.k_taps; j += kAppWarps) {
-      uint4 a[kGroup], b[kGroup];
+    for (int j0 = warp; j0 < p.k_taps; j0 += kAppWarps * kAhead) {
+      uint4 a[kAhead][kGroup], b[kAhead][kGroup];
 #pragma unroll
-      for (int g = 0; g < kGroup; ++g) {
-        a[g] = b[g] = make_uint4(0, 0, 0, 0);
-        if (g < ng && q0[g] + j >= 0) {
-          const uint16_t* src = state_row(p, k[g], q0[g] + j, lane);
-          a[g] = first_piece(src);
-          b[g] = second_piece(src);
+      for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+          const int j = j0 + kAppWarps * x;
+          a[x][g] = b[x][g] = make_uint4(0, 0, 0, 0);
+          if (g < ng && j < p.k_taps && q0[g] + j >= 0) {
+            const uint16_t* src = state_row(p, k[g], q0[g] + j, lane);
+            a[x][g] = first_piece(src);
+            b[x][g] = second_piece(src);
+          }
+        }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int j = min(j0 + kAppWarps * x, p.k_taps - 1);  // (past the last tap: zero rows)
+        const float4* wr = reinterpret_cast<const float4*>(p.w + size_t(j) * kD + 8 * lane);
+        const float4 w0 = __ldg(wr), w1 = __ldg(wr + 1), w2 = __ldg(wr + 64), w3 = __ldg(wr + 65);
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+          add8(acc[g], w0, w1, a[x][g]);
+          add8(acc[g] + 8, w2, w3, b[x][g]);
         }
       }
-      const float4* wr = reinterpret_cast<const float4*>(p.w + size_t(j) * kD + 8 * lane);
-      float4 w0 = __ldg(wr), w1 = __ldg(wr + 1);
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) add8(acc[g], w0, w1, a[g]);
-      w0 = __ldg(wr + 64);
-      w1 = __ldg(wr + 65);
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) add8(acc[g] + 8, w0, w1, b[g]);
     }
     if (r0) __syncthreads();  // the previous group's sums are read
 #pragma unroll
@@ -570,6 +580,36 @@ __global__ void __launch_bounds__(kAppThreads, 2)
   }
 }
 
+// The rows that a batch of long chunks leaves behind: the last window + k_taps tokens of every sequence into its raw
+// ring, the last `window` of them into the window cache.  One warp a row.
+template <int FMT>
+__global__ void __launch_bounds__(kAppThreads) append_rows_kernel(const __grid_constant__ AppendParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, r = blockIdx.x * kAppWarps + warp, R = p.window + p.k_taps;
+  const double theta = p.rope.theta_pi[lane];
+  pdl_trigger();
+  pdl_wait();
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  if (c0 < 0 || c1 > p.tokens || c1 - c0 > p.max_new || r >= min(c1 - c0, R)) return;  // (flagged by the entries' pass)
+  const int i = c1 - 1 - r;
+  const uint16_t* src = p.s_new + size_t(i) * kD + 8 * lane;
+  const uint4 v0 = first_piece(src), v1 = second_piece(src);
+  const int64_t at = __ldg(p.pos + i);
+  const int slot = __ldg(p.win_slot + i);
+  if (__ldg(p.seq + i) != b || at < i - c0 || at >= (int64_t(1) << 31) - p.lookahead - 1) return;
+  uint16_t* dst = p.ring + (size_t(b) * R + int(at) % R) * kD + 8 * lane;
+  *reinterpret_cast<uint4*>(dst) = v0;
+  *reinterpret_cast<uint4*>(dst + 256) = v1;
+  if (slot >= 0 && slot < p.win_rows) {
+    float x[kPer];
+    unpack8(v0, x);
+    unpack8(v1, x + 8);
+    to_consecutive(x, lane);
+    rotate_row(x, p, theta, int(at), lane);
+    store_row<FMT>(x, lane, slot, p.win_codes, p.win_scales);
+  }
+}
+
 template <int FMT, bool kLong>
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
@@ -581,12 +621,15 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
     mark_done_on_device(ready);
   }
   const dim3 grid(unsigned((p.tokens + p.per - 1) / p.per));
-  const bool entries = p.parts & kPartEntries;
-  const size_t smem = !entries ? 0 : kLong ? most : size_t(p.k_taps) * kD * sizeof(float);
+  const size_t smem = kLong ? most : size_t(p.k_taps) * kD * sizeof(float);
   return launch_pdl(append_paged_kernel<FMT, kLong>, grid, dim3(kAppThreads), smem, stream, p);
 }
 template <int FMT>
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+  if (!(p.parts & kPartEntries)) {
+    const dim3 grid(unsigned((p.window + p.k_taps + kAppWarps - 1) / kAppWarps), unsigned(p.batch));
+    return launch_pdl(append_rows_kernel<FMT>, grid, dim3(kAppThreads), 0, stream, p);
+  }
   return p.k_taps > kLongTaps ? launch_append<FMT, true>(p, stream) : launch_append<FMT, false>(p, stream);
 }
 
@@ -619,7 +662,12 @@ dsv4kv_status slot_map_launch(const int64_t* t_old, const int64_t* t_new, int ba
                      win_slot, comp_slot, static_cast<uint32_t*>(ws)};
   const int per = kSlotThreads * kSlotPer;
   const int grid = int(std::max<int64_t>(1, std::min<int64_t>(4 * sm_count(), (int64_t(capacity) + per - 1) / per)));
-  launch_pdl(slot_map_kernel, dim3(grid), dim3(kSlotThreads), size_t(batch + 1) * sizeof(int32_t), stream, p);
+  const size_t smem = size_t(3 * batch + 1) * sizeof(int32_t);
+  if (smem > 48 * 1024 - 256) {  // (more than 4070 sequences)
+    const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "slot_map_kernel: %s", cudaGetErrorString(e));
+  }
+  launch_pdl(slot_map_kernel, dim3(grid), dim3(kSlotThreads), smem, stream, p);
   return check_launch("slot_map_kernel");
 }
 
@@ -653,16 +701,13 @@ dsv4kv_status append_paged_launch(const void* s_new, const float* w, int batch, 
   p.comp_rows = comp.rows;
   p.status = static_cast<uint32_t*>(ws);
   rope_table_fill(&p.rope, rope_dim, rope_base);
-  // Few tokens: spread over the SMs.  Many: long entries (128 tokens apart in c128a) two CTAs an SM, so that up to four
-  // share a weight read; short ones in runs of at most 128 tokens; the rows of a second pass 32 tokens a CTA (they
-  // are the last ones of every sequence).
-  const bool lng = k_taps > kLongTaps;
-  const int64_t ctas = int64_t(lng ? 2 : 4) * sm_count();
+  // Few tokens: spread over the SMs; many: runs of up to 128 tokens (short entries), or long enough for two long
+  // entries (128 tokens apart in c128a) that share their weight reads.
+  const int64_t ctas = 4 * sm_count();
+  p.per = int(std::max<int64_t>(1, std::min<int64_t>((int64_t(tokens) + ctas - 1) / ctas, k_taps > kLongTaps ? kMaxTokens : 128)));
   const bool two = max_new > int64_t(lookahead) + 1;
   for (int pass = 0; pass < (two ? 2 : 1); ++pass) {
     p.parts = !two ? kPartEntries | kPartWindow | kPartRing : pass == 0 ? kPartEntries : kPartWindow | kPartRing;
-    p.per = int(std::max<int64_t>(1, std::min<int64_t>((int64_t(tokens) + ctas - 1) / ctas,
-                                                       pass == 1 ? 32 : lng ? kMaxTokens : 128)));
     cudaError_t e;
     switch (comp.fmt) {
       case DSV4KV_BF16: e = launch_append<DSV4KV_BF16>(p, stream); break;
