@@ -574,7 +574,7 @@ DSV4KV_API dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, 
     return set_error(DSV4KV_ERR_INVALID_ARG, "%s: bad sizes", what);
   if (lookahead < 0 || lookahead > window)
     return set_error(DSV4KV_ERR_INVALID_ARG, "%s: lookahead must be in [0, window]", what);
-  if (window > kMaxWindow || k_taps > kMaxWindow || stride > (1 << 24) || capacity >= (int64_t(1) << 31) - 4096)
+  if (batch > 4096 || window > kMaxWindow || k_taps > kMaxWindow || stride > (1 << 24) || capacity >= (int64_t(1) << 31) - 4096)
     return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: sizes too large", what);
   if (rope_dim < 0 || rope_dim > 512 || (rope_dim & 1))
     return set_error(DSV4KV_ERR_INVALID_ARG, "%s: rope_dim must be even and <= 512", what);

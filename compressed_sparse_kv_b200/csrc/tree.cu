@@ -76,7 +76,13 @@ constexpr uint32_t kColO = 0;    // O: 2 x 128 columns
 constexpr uint32_t kColS = 256;  // S: 2 buffers of 64 columns
 constexpr float kRaise = 8.0f;   // log2 units a score may pass the running maximum by
 constexpr float kNoMax = -1e30f;  // a maximum that nothing has reached yet
-constexpr int kSplitCost = 3;    // tiles that a cut group's partial sums and merge cost
+// Tiles that cut groups may cost (partial sums, a second part per pair, the merge) before whole groups take longer.
+// Whole groups of 10 tiles against runs of 7: 43 against 53 us; 12 against 7: 80 against 60; 10 against 6 (fp8): 89
+// against 71; 18 against 11 (fp8): 99 against 78.
+constexpr int kSplitCost = 3;
+// Row scales below this are taken as it: the weight of a stored row carries its scale and the denominator divides it
+// out again, which needs a normal reciprocal.  Such a row's values are below 2^-91.
+constexpr float kMinScale = 0x1p-100f;
 
 // Warps: 0 schedule and queries, 1 products, 2-5 keys, then the value loaders, then the softmax and epilogue.  bf16
 // rows need few loader threads (TMA, cp.async) and 16 softmax warps; quantised rows are converted by 8 loader warps,
@@ -1001,7 +1007,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         e.my[x] = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
         if (FMT == DSV4KV_FP4_E2M1_G16)
           e.mysc[x] = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
-        if (C::kRowScale) e.sr[x] = src ? static_cast<const float*>(src->scales)[row] : 0.f;
+        if (C::kRowScale) {
+          e.sr[x] = src ? static_cast<const float*>(src->scales)[row] : 1.f;
+          if (e.sr[x] == 0.f) e.my[x] = nullptr;  // a row of zeros
+        }
       }
     };
     while (ok && next_part()) {
@@ -1025,10 +1034,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           for (int x = 0; x < kX; ++x) {
             const int r = C::kValRows * vw + 32 * x + lane;
             if (C::kRowScale) {
-              const float sr = cur.sr[x];
-              inv = sr > 0.f ? __frcp_rn(sr) : 0.f;
+              const float sr = cur.sr[x], at_least = fmaxf(sr, kMinScale);
+              inv = 1.f / at_least;
               ctl->scale[sb][r] = sr;
-              ctl->lscale[sb][r] = sr > 0.f ? __log2f(sr) : 0.f;
+              ctl->lscale[sb][r] = __log2f(at_least);
               ctl->iscale[sb][r] = inv;
             }
             ctl->key[sb][r] = cur.key[x];
@@ -1115,8 +1124,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       if (FMT == DSV4KV_FP4_E2M1_G16)
         e.mysc = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
       if (C::kRowScale) {
-        const float sr = src ? static_cast<const float*>(src->scales)[row] : 0.f;
-        e.inv = sr > 0.f ? __frcp_rn(sr) : 0.f;
+        const float sr = src ? static_cast<const float*>(src->scales)[row] : 1.f;
+        e.inv = 1.f / fmaxf(sr, kMinScale);
+        if (sr == 0.f) e.my = nullptr;  // a row of zeros
       }
     };
     while (ok && next_part()) {

@@ -476,7 +476,7 @@ dsv4kv_status dsv4kv_slot_map(const int64_t* t_old, const int64_t* t_new, int32_
  *   rings after the entries are read.
  * cu, seq, pos, win_slot, comp_slot: as dsv4kv_slot_map writes them with the
  * same window, stride and lookahead.  The two caches have one format; their
- * tables are not read.  Requirements: dim == 512; rope_dim even, <= 512
+ * tables are not read.  Requirements: dim == 512; batch <= 4096; rope_dim even, <= 512
  * (64 with DSV4KV_FP8_E4M3_ROW_ROPE_BF16); 0 <= lookahead <= window; win may be
  * NULL when window == 0; workspace as dsv4kv_block_table_update.
  * ------------------------------------------------------------------------ */
@@ -518,6 +518,7 @@ dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t bat
  * sets DSV4KV_DEV_BAD_LENGTH; a parent outside [-1, i) is taken as -1 and sets
  * DSV4KV_DEV_BAD_TREE.  Rows no node of the call attends to are not read;
  * infinities and NaN in rows that one node does not see stay out of its output.
+ * fp8 row scales are taken as at least 2^-100 (0: a row of zeros).
  * Requirements: dim == 512; 1 <= heads <= 128; 1 <= max_nodes <= 256;
  * nodes * heads < 2^31; 1 <= batch <= 1024; the three caches of one format;
  * 1 <= k <= 2048 with idx; stride >= 1; 0 <= window <= 65536; t_max < 2^30.

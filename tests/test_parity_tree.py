@@ -198,3 +198,74 @@ def test_two_streams_at_once():
         got = a.run(stream=s[0]), b.run(stream=s[1])
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_tiny_and_zero_row_scales():
+    """Rows whose fp8 scale is 0 (a row of zeros), below the smallest normal number or many powers of two below the
+    others' keep their place in the softmax."""
+    c = TreeCase(120, [900, 300], [4, 3], 16, K.FP8_E4M3_ROW, stride=4)
+    for b, (t, vals) in enumerate(zip(c.ts, c.comp_v)):
+        for r, scale in ((3, 0.0), (5, 2.0 ** -140), (9, 2.0 ** -60), (20, 2.0 ** -90)):
+            at = int(c.comp.table[b, r // 64]) * 64 + r % 64
+            vals[r] *= scale / float(c.comp.scales[at])
+            c.comp.scales[at] = scale
+    c.check(c.run())
+
+
+def test_rows_past_four_gib_of_the_pool():
+    """Pages at the end of a pool of more than 2^32 bytes."""
+    c = TreeCase(121, [9000, 200], [3, 2], 64, K.BF16, stride=4, page=64)
+    rows, far = c.comp.codes.shape[0], (5 << 30) // 1024 // 64 * 64
+    pool = torch.empty(far + rows, 512, dtype=torch.bfloat16, device="cuda")
+    pool[far:] = c.comp.codes
+    table = torch.where(c.comp.table >= 0, c.comp.table + far // 64, -1).to(torch.int32)
+    c.comp = K.PagedCache(K.BF16, pool, table, 64)
+    c.check(c.run())
+    s = TreeCase(122, [9000], [3], 16, K.BF16, stride=4, page=64, k=40)
+    pool = torch.empty(far + s.comp.codes.shape[0], 512, dtype=torch.bfloat16, device="cuda")
+    pool[far:] = s.comp.codes
+    s.comp = K.PagedCache(K.BF16, pool, torch.where(s.comp.table >= 0, s.comp.table + far // 64, -1).to(torch.int32), 64)
+    s.check(s.run())
+
+
+def test_a_selected_entry_named_twice_counts_twice():
+    c = TreeCase(123, [900], [2], 16, K.BF16, stride=4, k=6)
+    c.idx[0] = torch.tensor([7, 7, 7, 3, 190, -1], dtype=torch.int32)
+    c.idx_v[0][0] = [7, 7, 7, 3, 190]
+    c.check(c.run())
+
+
+def test_no_drafted_nodes_at_all():
+    c = TreeCase(124, [900, 10], [2, 3], 16, K.BF16, stride=4)
+    out = torch.full((c.rows, 16, 512), 3.0, device="cuda")
+    ws = c.workspace()
+    c.cu_d.zero_()
+    c.run(ws=ws, out=out)
+    assert torch.all(out == 3.0) and K.workspace_status(ws) == 0
+
+
+def test_a_large_batch():
+    rng = np.random.default_rng(5)
+    b = 1024
+    c = TreeCase(125, [int(t) for t in rng.integers(0, 400, b)], [int(m) for m in rng.integers(0, 3, b)], 4, K.BF16, stride=4)
+    both(c)
+
+
+def test_two_graphs_share_a_workspace():
+    a, b = TreeCase(126, [20000], [2], 64, K.BF16, stride=4), TreeCase(127, [16000, 300], [1, 3], 64, K.BF16, stride=4)
+    ws = K.new_workspace(max(a.workspace().numel(), b.workspace().numel()))
+    outs, graphs = [], []
+    for c in (a, b):
+        out = torch.empty(c.rows, 64, 512, device="cuda")
+        c.run(ws=ws, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(ws=ws, out=out)
+        outs.append(out)
+        graphs.append(g)
+    for k in (0, 1, 0, 0, 1):
+        outs[k].zero_()
+        graphs[k].replay()
+        (a, b)[k].check(outs[k])
+    assert K.workspace_status(ws) == 0
