@@ -322,7 +322,7 @@ DSV4KV_API dsv4kv_status dsv4kv_sparse_decode(const void* q, const dsv4kv_cache*
 // Checks a paged cache whose sequences have at most `max_rows` rows and
 // turns it into the kernels' form (a pool "cache" of pool rows + its pages).
 static dsv4kv_status check_paged(const dsv4kv_paged_cache* c, const char* what, int64_t max_rows, int dim,
-                                 bool keys, dsv4kv_cache* pool, PageDesc* pg) {
+                                 bool keys, dsv4kv_cache* pool, PageDesc* pg, int min_pages = 1) {
   if (!c) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: paged cache descriptor is null", what);
   if (c->dim != dim) return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: dim %d, expected %d", what, c->dim, dim);
   if (keys ? (c->fmt != DSV4KV_BF16 && c->fmt != DSV4KV_FP4_E2M1_G16)
@@ -330,7 +330,7 @@ static dsv4kv_status check_paged(const dsv4kv_paged_cache* c, const char* what, 
     return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: format %d", what, c->fmt);
   if (c->page_rows <= 0 || c->page_rows % 64 != 0)
     return set_error(DSV4KV_ERR_INVALID_ARG, "%s: page_rows must be a positive multiple of 64", what);
-  if (c->pool_pages < 1 || c->pool_pages * int64_t(c->page_rows) >= (int64_t(1) << 31))
+  if (c->pool_pages < min_pages || c->pool_pages * int64_t(c->page_rows) >= (int64_t(1) << 31))
     return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the pool must hold between 1 page and 2^31 rows", what);
   const int64_t need_pages = (max_rows + c->page_rows - 1) / c->page_rows;
   if (c->table_stride < need_pages)
@@ -492,10 +492,10 @@ static int64_t step_rows(int64_t t, int32_t window, int32_t stride, int32_t look
 }
 
 static dsv4kv_status check_table(const char* what, const int32_t* table, int32_t page_rows, int32_t table_stride,
-                                 int64_t pool_pages, int64_t max_rows) {
+                                 int64_t pool_pages, int64_t max_rows, int min_pages) {
   if (page_rows <= 0 || page_rows % 64 != 0)
     return set_error(DSV4KV_ERR_INVALID_ARG, "%s: page_rows must be a positive multiple of 64", what);
-  if (pool_pages < 1 || pool_pages > ((int64_t(1) << 31) - 1) / page_rows)
+  if (pool_pages < min_pages || pool_pages > ((int64_t(1) << 31) - 1) / page_rows)
     return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: the pool must hold between 1 page and 2^31 rows", what);
   const int64_t need = (max_rows + page_rows - 1) / page_rows;
   if (table_stride < need)
@@ -517,7 +517,7 @@ DSV4KV_API dsv4kv_status dsv4kv_block_table_update(const int64_t* t_old, const i
   if (st != DSV4KV_OK) return st;
   if (stride < 0) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: stride < 0", what);
   const int64_t rows = step_rows(t_max, window, stride, lookahead);
-  st = check_table(what, table, page_rows, table_stride, pool_pages, rows);
+  st = check_table(what, table, page_rows, table_stride, pool_pages, rows, rows > 0);
   if (st != DSV4KV_OK) return st;
   if (int64_t(batch) * ((rows + page_rows - 1) / page_rows) >= (int64_t(1) << 31))
     return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: batch x pages must be < 2^31", what);
@@ -547,13 +547,14 @@ DSV4KV_API dsv4kv_status dsv4kv_slot_map(const int64_t* t_old, const int64_t* t_
   PageDesc cp{nullptr, 64, 0, 0}, wp{nullptr, 64, 0, 0};
   if (comp) {
     st = check_table(what, comp->table, comp->page_rows, comp->table_stride, comp->pool_pages,
-                     step_rows(t_max, window, stride, lookahead));
+                     step_rows(t_max, window, stride, lookahead),
+                     step_rows(t_max, window, stride, lookahead) > 0);
     if (st != DSV4KV_OK) return st;
     cp = PageDesc{comp->table, comp->page_rows, comp->table_stride, comp->pool_pages};
   }
   if (window > 0) {
     st = check_table(what, win->table, win->page_rows, win->table_stride, win->pool_pages,
-                     std::min<int64_t>(t_max, window));
+                     std::min<int64_t>(t_max, window), t_max > 0);
     if (st != DSV4KV_OK) return st;
     wp = PageDesc{win->table, win->page_rows, win->table_stride, win->pool_pages};
   }
@@ -593,7 +594,7 @@ DSV4KV_API dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, 
     if (!c) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: paged cache descriptor is null", what);
     if (c->fmt < DSV4KV_BF16 || c->fmt > DSV4KV_FP8_E4M3_ROW_ROPE_BF16)
       return set_error(DSV4KV_ERR_UNSUPPORTED, "%s: format %d", what, c->fmt);
-    dsv4kv_status st = check_table(what, c->table, c->page_rows, c->table_stride, c->pool_pages, 0);
+    dsv4kv_status st = check_table(what, c->table, c->page_rows, c->table_stride, c->pool_pages, 0, 1);
     if (st != DSV4KV_OK) return st;
     pool[i] = dsv4kv_cache{c->fmt, c->dim, c->pool_pages * int64_t(c->page_rows), c->codes, c->scales};
     st = check_cache(&pool[i], what, 1, 512);
@@ -650,9 +651,9 @@ DSV4KV_API dsv4kv_status dsv4kv_tree_decode_paged(const void* q, const dsv4kv_pa
   const int32_t w_max = int32_t(std::min<int64_t>(t_max, window));
   dsv4kv_cache cpool{}, wpool{};
   PageDesc cpg{}, wpg{};
-  st = check_paged(comp, what, dsv4kv_compress_entries(t_max, window, stride), 512, false, &cpool, &cpg);
+  st = check_paged(comp, what, dsv4kv_compress_entries(t_max, window, stride), 512, false, &cpool, &cpg, n_max > 0);
   if (st != DSV4KV_OK) return st;
-  st = check_paged(win, what, w_max, 512, false, &wpool, &wpg);
+  st = check_paged(win, what, w_max, 512, false, &wpool, &wpg, w_max > 0);
   if (st != DSV4KV_OK) return st;
   if (n_max > 0) {  // (table entries past table_stride are bad pages to the kernel)
     if (!cpg.table) return set_error(DSV4KV_ERR_INVALID_ARG, "%s: block table is null", what);

@@ -627,7 +627,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
 template <int FMT>
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   if (!(p.parts & kPartEntries)) {
-    const dim3 grid(unsigned((p.window + p.k_taps + kAppWarps - 1) / kAppWarps), unsigned(p.batch));
+    const dim3 grid(unsigned((std::min(p.window + p.k_taps, p.max_new) + kAppWarps - 1) / kAppWarps), unsigned(p.batch));
     return launch_pdl(append_rows_kernel<FMT>, grid, dim3(kAppThreads), 0, stream, p);
   }
   return p.k_taps > kLongTaps ? launch_append<FMT, true>(p, stream) : launch_append<FMT, false>(p, stream);

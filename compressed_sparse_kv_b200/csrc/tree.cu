@@ -75,7 +75,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;    // O: 2 x 128 columns
 constexpr uint32_t kColS = 256;  // S: 2 buffers of 64 columns
 constexpr float kRaise = 8.0f;   // log2 units a score may pass the running maximum by
-constexpr float kNoMax = -1e30f;  // a maximum that nothing has reached yet
+constexpr float kNoMax = -3.4028235e38f;  // a maximum that nothing has reached yet (finite: x - m of a hidden row is -inf)
 // Tiles that cut groups may cost (partial sums, a second part per pair, the merge) before whole groups take longer.
 // Whole groups of 10 tiles against runs of 7: 43 against 53 us; 12 against 7: 80 against 60; 10 against 6 (fp8): 89
 // against 71; 18 against 11 (fp8): 99 against 78.
@@ -1009,7 +1009,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           e.mysc[x] = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
         if (C::kRowScale) {
           e.sr[x] = src ? static_cast<const float*>(src->scales)[row] : 1.f;
-          if (e.sr[x] == 0.f) e.my[x] = nullptr;  // a row of zeros
+          if (e.sr[x] == 0.f) {  // a row of zeros
+            e.sr[x] = 1.f;
+            e.my[x] = nullptr;
+          }
         }
       }
     };
@@ -1357,9 +1360,11 @@ dsv4kv_status tree_decode_launch(const TreeArgs& a, void* ws, cudaStream_t strea
   if (!encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 64, uint64_t(a.nodes) * a.heads, 8, kDim * 2, 128, 64, kQ,
                       8, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(DSV4KV_ERR_CUDA, "tree_decode_paged: tensor map of q");
-  if (a.comp.fmt == DSV4KV_BF16 && a.comp.codes &&
-      !encode_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.comp.codes, 64, uint64_t(a.comp.rows), 8, kDim * 2, 128, 64,
-                      64, 4, CU_TENSOR_MAP_SWIZZLE_128B))
+  // (no sequence of a pool without pages has a row to load: any valid map serves)
+  const bool none = !a.comp.codes || a.comp.rows == 0;
+  if (a.comp.fmt == DSV4KV_BF16 &&
+      !encode_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, none ? a.q : a.comp.codes, 64, none ? 1 : uint64_t(a.comp.rows),
+                      8, kDim * 2, 128, 64, 64, 4, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(DSV4KV_ERR_CUDA, "tree_decode_paged: tensor map of the compressed cache");
   cudaError_t e;
   switch (a.comp.fmt) {

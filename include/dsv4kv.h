@@ -405,8 +405,8 @@ dsv4kv_status dsv4kv_dense_decode_paged(const void* q, const dsv4kv_paged_cache*
  * `lookahead` (0 <= lookahead <= window) also makes room for the entries that
  * drafted tokens up to that many positions ahead attend to (dsv4kv_append_paged).
  * Requirements: 0 <= batch <= 4096; t_max < 2^30; page_rows a positive
- * multiple of 64; table_stride >= pages(t_max); pool_pages * page_rows < 2^31;
- * batch * pages(t_max) < 2^31.
+ * multiple of 64; table_stride >= pages(t_max); pool_pages * page_rows < 2^31,
+ * and pool_pages >= 1 unless pages(t_max) == 0; batch * pages(t_max) < 2^31.
  * Workspace: dsv4kv_paged_step_workspace_bytes.
  * ------------------------------------------------------------------------ */
 size_t dsv4kv_paged_step_workspace_bytes(int32_t batch);
@@ -517,10 +517,12 @@ dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t bat
  * descends, exceeds `nodes` or makes a tree larger than max_nodes is clamped and
  * sets DSV4KV_DEV_BAD_LENGTH; a parent outside [-1, i) is taken as -1 and sets
  * DSV4KV_DEV_BAD_TREE.  Rows no node of the call attends to are not read;
- * infinities and NaN in rows that one node does not see stay out of its output.
+ * infinities and NaN in rows that one node does not see stay out of its output
+ * (a row that it sees with a score of -infinity weighs nothing).
  * fp8 row scales are taken as at least 2^-100 (0: a row of zeros).
  * Requirements: dim == 512; 1 <= heads <= 128; 1 <= max_nodes <= 256;
- * nodes * heads < 2^31; 1 <= batch <= 1024; the three caches of one format;
+ * nodes * heads < 2^31; a pool of no pages only where no sequence up to t_max
+ * can have a row of it; 1 <= batch <= 1024; the three caches of one format;
  * 1 <= k <= 2048 with idx; stride >= 1; 0 <= window <= 65536; t_max < 2^30.
  * ------------------------------------------------------------------------ */
 /* (k = 0: the dense form, idx NULL) */

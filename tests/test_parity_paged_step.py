@@ -335,3 +335,52 @@ def test_a_serving_loop_in_one_graph():
             assert np.linalg.norm(got[lo:lo + M] - ref) <= 5e-3 * np.linalg.norm(ref)
     used = sum(-(-S.cache_rows(x, W, s, L) // page) for x in t)
     assert count.item() == pool - used
+
+
+def test_a_pool_without_a_page():
+    """No sequence is long enough for a compressed entry, nor has a page for one."""
+    old, new = dev([0, 50], torch.int64), dev([9, 100], torch.int64)
+    ws = K.new_workspace(K.paged_step_workspace_bytes(2))
+    pages, wpages = K.PageTable(dev([[-1], [-1]]), 64, 0), K.PageTable(dev([[2, 0], [1, 3]]), 64, 4)
+    count = dev([0], torch.int64)
+    K.block_table_update(old, new, pages, dev([]), count, t_max=100, window=128, stride=4, lookahead=16,
+                         free_count_out=count, ws=ws)
+    m = K.slot_map(old, new, pages, wpages, 64, 100, window=128, stride=4, lookahead=16, ws=ws)
+    assert K.workspace_status(ws) == 0 and count.item() == 0 and pages.table.tolist() == [[-1], [-1]]
+    assert m.cu.tolist() == [0, 9, 59]
+    want = [128 + i for i in range(9)] + [64 + p if p < 64 else 192 + p - 64 for p in range(50, 100)]
+    assert m.win_slot[:59].tolist() == want and torch.all(m.comp_slot[:59] < 0)
+
+
+def test_the_largest_batch():
+    """4096 sequences, most of them idle, from tables to cache rows."""
+    B, W, page = 4096, 128, 64
+    rng = np.random.default_rng(8)
+    t_old = rng.integers(0, 600, B)
+    t_new = t_old + np.where(rng.random(B) < 0.1, rng.integers(1, 40, B), 0)
+    table, free, pool = step_case(8, t_old.tolist(), t_new.tolist(), page, W, 4, 0)
+    want_t, want_f = S.block_table_update(t_old.tolist(), t_new.tolist(), table, free, page, W, 4, 0)
+    wt = rng.permutation(2 * B).reshape(B, 2)
+    comp = K.PagedCache(0, torch.zeros(pool * page, 512, dtype=torch.bfloat16, device="cuda"), dev(table), page)
+    win = K.PagedCache(0, torch.zeros(2 * B * page, 512, dtype=torch.bfloat16, device="cuda"), dev(wt.tolist()), page)
+    ws, count = K.new_workspace(K.paged_step_workspace_bytes(B)), dev([len(free)], torch.int64)
+    old, new, fl = dev(t_old.tolist(), torch.int64), dev(t_new.tolist(), torch.int64), dev(free)
+    cap, t_max = int((t_new - t_old).sum()), int(t_new.max())
+    K.block_table_update(old, new, K.PageTable(comp.table, page, pool), fl, count, t_max=t_max, window=W, stride=4,
+                         lookahead=0, free_count_out=count, ws=ws)
+    assert comp.table.tolist() == want_t and count.item() == len(want_f)
+    m = K.slot_map(old, new, K.PageTable(comp.table, page, pool), K.PageTable(win.table, page, 2 * B), cap, t_max,
+                   window=W, stride=4, lookahead=0, ws=ws)
+    want_seq = np.repeat(np.arange(B), t_new - t_old)
+    want_pos = np.concatenate([np.arange(a, b) for a, b in zip(t_old, t_new)])
+    assert np.array_equal(m.seq.cpu().numpy(), want_seq) and np.array_equal(m.pos.cpu().numpy(), want_pos)
+    w = torch.zeros(8, 512, device="cuda")
+    w[7] = 1.0                                   # an entry is its last tap's state
+    ring = torch.zeros(B, W + 8, 512, dtype=torch.bfloat16, device="cuda")
+    x = dev(rng.integers(1, 200, cap).tolist(), torch.bfloat16)[:, None].expand(cap, 512).contiguous()
+    K.append_paged(x, w, m, ring, win, comp, stride=4, window=W, lookahead=0, max_new=40, rope_dim=0, ws=ws)
+    assert K.workspace_status(ws) == 0
+    seq, pos = torch.from_numpy(want_seq).cuda(), torch.from_numpy(want_pos).cuda()
+    assert torch.equal(ring[seq, pos % (W + 8)], x)
+    at = win.table[seq, (pos % W) // page].long() * page + pos % W % page
+    assert torch.equal(win.codes[at], x)

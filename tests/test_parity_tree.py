@@ -269,3 +269,40 @@ def test_two_graphs_share_a_workspace():
         graphs[k].replay()
         (a, b)[k].check(outs[k])
     assert K.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("k", [0, 8])
+def test_pools_without_a_page(fmt, k):
+    """Contexts too short for a compressed entry need no pool, empty ones no window pool either."""
+    c = TreeCase(128, [100, 12], [3, 5], 16, fmt, stride=128)
+    empty = lambda x: K.PagedCache(fmt, x.codes[:0], x.table, x.page_rows, None if x.scales is None else x.scales[:0])  # noqa: E731
+    c.comp = empty(c.comp)
+    if k:
+        c.k, c.idx, c.idx_v = k, torch.full((c.rows, k), -1, dtype=torch.int32, device="cuda"), [[[]] * m for m in c.ms]
+        c.idx[1, 0] = 0                     # (not an entry of that node)
+    c.check(c.run())
+    c = TreeCase(129, [0, 0], [3, 5], 16, fmt, stride=128)
+    c.comp, c.win = empty(c.comp), empty(c.win)
+    c.check(c.run())
+
+
+def test_scores_near_the_lowest_number():
+    """One row, whose score is far below -1e30 for half of the heads, has all the weight."""
+    def large(comp, win, draft):
+        win[0][:] = 1e17
+    c = TreeCase(130, [1], [1], 16, K.BF16, q_scale=1e17, edit=large)
+    assert ((c.q_v @ c.win_v[0].T).min()) < -1e35
+    both(c)
+
+
+def test_zero_rows_beside_large_scales():
+    """A row of zeros counts in the denominator however large the other rows' scales are."""
+    def large(comp, win, draft):
+        comp[0] *= 2.0 ** 12
+    c = TreeCase(131, [900], [2], 16, K.FP8_E4M3_ROW, stride=4, q_scale=2.0 ** -12, edit=large)
+    for r in range(0, len(c.comp_v[0]), 2):
+        at = int(c.comp.table[0, r // 64]) * 64 + r % 64
+        c.comp_v[0][r] = 0.0
+        c.comp.scales[at] = 0.0
+    both(c)
