@@ -293,12 +293,11 @@ struct Tok {
   int i, b, pos, first, slot;  // token, sequence, position, the sequence's first new token, its entry's pool row
 };
 
-// While rows are loaded and summed a lane holds channels [8 lane, 8 lane + 8) and [256 + 8 lane, ..), so that every load
-// of a row is one contiguous 512-byte piece; rotation and storing want channels [16 lane, 16 lane + 16).
-__device__ __forceinline__ void to_consecutive(float (&x)[kPer], int lane) {
+// A lane holds channels [8 lane, 8 lane + 8) and [256 + 8 lane, ..) of a row, so that every load of it (and store of a
+// bf16 row) is one contiguous 512-byte piece; the quantisers want channels [16 lane, 16 lane + 16).
+__device__ __forceinline__ void to_consecutive(const float (&x)[kPer], float (&y)[kPer], int lane) {
   const int from = (2 * lane) & 31;  // the lane that holds 8-channel pieces 2 lane (2 lane + 1: the next one)
   const bool upper = lane >= 16;     // of the upper 256 channels
-  float y[kPer];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float a0 = __shfl_sync(kFull, x[e], from), a1 = __shfl_sync(kFull, x[8 + e], from);
@@ -306,32 +305,29 @@ __device__ __forceinline__ void to_consecutive(float (&x)[kPer], int lane) {
     y[e] = upper ? a1 : a0;
     y[8 + e] = upper ? b1 : b0;
   }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) x[e] = y[e];
 }
 
-// x = channels [16 lane, 16 lane + 16) of a row, its rotary pairs rotated at pos.
-// theta: pair `lane`'s theta / pi (where there are at most 32 pairs).
+// Rotates a row's rotary pairs at pos.  theta: pair `lane`'s theta / pi (where there are at most 32 pairs).
 __device__ __forceinline__ void rotate_row(float (&x)[kPer], const AppendParams& p, double theta, int pos, int lane) {
-  const int r0 = kD - p.rope_dim, pairs = p.rope_dim / 2, c0 = kPer * lane;
+  const int r0 = kD - p.rope_dim, pairs = p.rope_dim / 2;
   if (pairs <= 32) {
-    // lane m computes pair m; the lanes that own rotary channels fetch theirs
+    // lane m computes pair m; the lanes that own rotary channels (of the second piece) fetch theirs
     float cs_m = 1.f, sn_m = 0.f;
     if (lane < pairs) rope_rotation(theta, double(pos), &cs_m, &sn_m);
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) {
-      const int m = (c0 + e - r0) >> 1;
+    for (int e = 0; e < 8; e += 2) {
+      const int m = (256 + 8 * lane + e - r0) >> 1;
       const float cs = __shfl_sync(kFull, cs_m, m & 31), sn = __shfl_sync(kFull, sn_m, m & 31);
       if (m >= 0) {
-        const float a = x[e], b = x[e + 1];
-        x[e] = a * cs - b * sn;
-        x[e + 1] = a * sn + b * cs;
+        const float a = x[8 + e], b = x[9 + e];
+        x[8 + e] = a * cs - b * sn;
+        x[9 + e] = a * sn + b * cs;
       }
     }
   } else {
 #pragma unroll
     for (int e = 0; e < kPer; e += 2) {
-      const int m = (c0 + e - r0) >> 1;
+      const int m = ((e < 8 ? 8 * lane + e : 248 + 8 * lane + e) - r0) >> 1;
       if (m >= 0) {
         float cs, sn;
         rope_rotation(p.rope.theta_pi[m], double(pos), &cs, &sn);
@@ -346,14 +342,16 @@ __device__ __forceinline__ void rotate_row(float (&x)[kPer], const AppendParams&
 template <int FMT>
 __device__ __forceinline__ void store_row(const float (&x)[kPer], int lane, int64_t row, uint8_t* codes, void* scales) {
   if constexpr (FMT == DSV4KV_BF16) {
-    uint16_t* dst = reinterpret_cast<uint16_t*>(codes) + size_t(row) * kD + kPer * lane;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(codes) + size_t(row) * kD + 8 * lane;
 #pragma unroll
-    for (int q = 0; q < kPer / 8; ++q)
-      *reinterpret_cast<uint4*>(dst + 8 * q) =
+    for (int q = 0; q < 2; ++q)
+      *reinterpret_cast<uint4*>(dst + 256 * q) =
           make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
                      pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
   } else {
-    quantize_row<kPer, FMT>(x, lane, size_t(row), codes, scales);
+    float y[kPer];
+    to_consecutive(x, y, lane);
+    quantize_row<kPer, FMT>(y, lane, size_t(row), codes, scales);
   }
 }
 
@@ -374,11 +372,33 @@ __device__ __forceinline__ const uint16_t* state_row(const AppendParams& p, cons
 __device__ __forceinline__ uint4 first_piece(const uint16_t* row) { return *reinterpret_cast<const uint4*>(row); }
 __device__ __forceinline__ uint4 second_piece(const uint16_t* row) { return *reinterpret_cast<const uint4*>(row + 256); }
 
-__device__ __forceinline__ void add8(float* acc, const float4& w0, const float4& w1, const uint4& v) {
-  acc[0] = fmaf(w0.x, bf16lo(v.x), acc[0]); acc[1] = fmaf(w0.y, bf16hi(v.x), acc[1]);
-  acc[2] = fmaf(w0.z, bf16lo(v.y), acc[2]); acc[3] = fmaf(w0.w, bf16hi(v.y), acc[3]);
-  acc[4] = fmaf(w1.x, bf16lo(v.z), acc[4]); acc[5] = fmaf(w1.y, bf16hi(v.z), acc[5]);
-  acc[6] = fmaf(w1.z, bf16lo(v.w), acc[6]); acc[7] = fmaf(w1.w, bf16hi(v.w), acc[7]);
+// Sums of channel pairs: one packed fused multiply-add (each half rounded as fmaf rounds) for two channels.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 pair_value(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void add2(uint64_t& acc, uint64_t w, uint32_t v) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(w), "l"(pair_of(bf16lo(v), bf16hi(v))));
+}
+__device__ __forceinline__ void add8(uint64_t* acc, const ulonglong2& w0, const ulonglong2& w1, const uint4& v) {
+  add2(acc[0], w0.x, v.x);
+  add2(acc[1], w0.y, v.y);
+  add2(acc[2], w1.x, v.z);
+  add2(acc[3], w1.y, v.w);
+}
+__device__ __forceinline__ void sums_of(const uint64_t (&acc)[kPer / 2], float (&x)[kPer]) {
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) {
+    const float2 v = pair_value(acc[e]);
+    x[2 * e] = v.x;
+    x[2 * e + 1] = v.y;
+  }
 }
 
 // Appends i to list[n ..] where `keep`, in thread order; returns the new length.  All threads call it.
@@ -459,7 +479,6 @@ __global__ void __launch_bounds__(kAppThreads, 2)
       float x[kPer];
       unpack8(v0, x);
       unpack8(v1, x + 8);
-      to_consecutive(x, lane);
       rotate_row(x, p, theta, k.pos, lane);
       store_row<FMT>(x, lane, slot, p.win_codes, p.win_scales);
     }
@@ -467,10 +486,10 @@ __global__ void __launch_bounds__(kAppThreads, 2)
   if constexpr (!kLong) {
     if (n_ents == 0) return;
     // weights [tap][quarter][lane] float4: a lane's two pieces of 8 channels in four conflict-free reads
-    float4* sw = reinterpret_cast<float4*>(red);
+    ulonglong2* sw = reinterpret_cast<ulonglong2*>(red);
     for (int i = threadIdx.x; i < p.k_taps * (kD / 4); i += kAppThreads) {
       const int j = i / (kD / 4), c = i % (kD / 4);  // quad c: lane (c / 2) % 32, quarter 2 (c / 64) + c % 2
-      sw[(j * 4 + 2 * (c >> 6) + (c & 1)) * 32 + ((c >> 1) & 31)] = reinterpret_cast<const float4*>(p.w)[i];
+      sw[(j * 4 + 2 * (c >> 6) + (c & 1)) * 32 + ((c >> 1) & 31)] = reinterpret_cast<const ulonglong2*>(p.w)[i];
     }
     __syncthreads();
     // consecutive entries to one warp: the rows that two entries share come from L1 the second time
@@ -481,32 +500,48 @@ __global__ void __launch_bounds__(kAppThreads, 2)
       const Tok k = next;
       if (r + 1 < end) next = token(ents[r + 1]);
       const int q0 = k.pos + 1 + p.lookahead - p.window - p.k_taps;
-      float acc[kPer];
+      const int i0 = k.i - (k.pos - q0);  // the first tap's token
+      uint64_t acc[kPer / 2];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+      for (int e = 0; e < kPer / 2; ++e) acc[e] = 0;
+      auto add = [&](int j, const uint4& a, const uint4& b) {
+        const ulonglong2* w = sw + j * 128 + lane;
+        add8(acc, w[0], w[32], a);
+        add8(acc + 4, w[64], w[96], b);
+      };
+      int j0 = max(0, -q0);
+      if (i0 >= k.first) {  // all taps are new tokens: consecutive rows
+        const uint16_t* src = p.s_new + size_t(i0) * kD + 8 * lane;
 #pragma unroll 2
-      for (int j0 = max(0, -q0); j0 < p.k_taps; j0 += 4) {
+        for (; j0 + 4 <= p.k_taps; j0 += 4) {
+          uint4 a[4], b[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            a[x] = first_piece(src + (j0 + x) * kD);
+            b[x] = second_piece(src + (j0 + x) * kD);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) add(j0 + x, a[x], b[x]);
+        }
+      }
+#pragma unroll 1
+      for (; j0 < p.k_taps; j0 += 4) {
         uint4 a[4], b[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          a[x] = b[x] = make_uint4(0, 0, 0, 0);
-          if (j0 + x < p.k_taps) {
-            const uint16_t* src = state_row(p, k, q0 + j0 + x, lane);
-            a[x] = first_piece(src);
-            b[x] = second_piece(src);
-          }
+          if (j0 + x >= p.k_taps) break;
+          const uint16_t* src = state_row(p, k, q0 + j0 + x, lane);
+          a[x] = first_piece(src);
+          b[x] = second_piece(src);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (j0 + x >= p.k_taps) break;
-          const float4* w = sw + (j0 + x) * 128 + lane;
-          add8(acc, w[0], w[32], a[x]);
-          add8(acc + 8, w[64], w[96], b[x]);
-        }
+        for (int x = 0; x < 4; ++x)
+          if (j0 + x < p.k_taps) add(j0 + x, a[x], b[x]);
       }
-      to_consecutive(acc, lane);
-      rotate_row(acc, p, theta, q0 + p.k_taps - p.stride, lane);
-      store_row<FMT>(acc, lane, k.slot, p.comp_codes, p.comp_scales);
+      float x[kPer];
+      sums_of(acc, x);
+      rotate_row(x, p, theta, q0 + p.k_taps - p.stride, lane);
+      store_row<FMT>(x, lane, k.slot, p.comp_codes, p.comp_scales);
     }
     return;
   }
@@ -514,13 +549,13 @@ __global__ void __launch_bounds__(kAppThreads, 2)
     const int ng = min(kGroup, n_ents - r0);
     Tok k[kGroup];
     int q0[kGroup];
-    float acc[kGroup][kPer];
+    uint64_t acc[kGroup][kPer / 2];
 #pragma unroll
     for (int g = 0; g < kGroup; ++g) {
       k[g] = token(ents[min(r0 + g, n_ents - 1)]);
       q0[g] = k[g].pos + 1 + p.lookahead - p.window - p.k_taps;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[g][e] = 0.f;
+      for (int e = 0; e < kPer / 2; ++e) acc[g][e] = 0;
     }
 #pragma unroll 1
     for (int j0 = warp; j0 < p.k_taps; j0 += kAppWarps * kAhead) {
@@ -540,12 +575,12 @@ __global__ void __launch_bounds__(kAppThreads, 2)
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) {
         const int j = min(j0 + kAppWarps * x, p.k_taps - 1);  // (past the last tap: zero rows)
-        const float4* wr = reinterpret_cast<const float4*>(p.w + size_t(j) * kD + 8 * lane);
-        const float4 w0 = __ldg(wr), w1 = __ldg(wr + 1), w2 = __ldg(wr + 64), w3 = __ldg(wr + 65);
+        const ulonglong2* wr = reinterpret_cast<const ulonglong2*>(p.w + size_t(j) * kD + 8 * lane);
+        const ulonglong2 w0 = __ldg(wr), w1 = __ldg(wr + 1), w2 = __ldg(wr + 64), w3 = __ldg(wr + 65);
 #pragma unroll
         for (int g = 0; g < kGroup; ++g) {
           add8(acc[g], w0, w1, a[x][g]);
-          add8(acc[g] + 8, w2, w3, b[x][g]);
+          add8(acc[g] + 4, w2, w3, b[x][g]);
         }
       }
     }
@@ -555,8 +590,10 @@ __global__ void __launch_bounds__(kAppThreads, 2)
       if (g >= ng) break;
       float4* dst = reinterpret_cast<float4*>(red + (size_t(warp) * kGroup + g) * kD) + lane;
 #pragma unroll
-      for (int q = 0; q < kPer / 4; ++q)  // (conflict-free: quarter q of every lane side by side)
-        dst[32 * q] = make_float4(acc[g][4 * q], acc[g][4 * q + 1], acc[g][4 * q + 2], acc[g][4 * q + 3]);
+      for (int q = 0; q < kPer / 4; ++q) {  // (conflict-free: quarter q of every lane side by side)
+        const float2 lo = pair_value(acc[g][2 * q]), hi = pair_value(acc[g][2 * q + 1]);
+        dst[32 * q] = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
     __syncthreads();
     if (warp < ng) {
@@ -572,7 +609,6 @@ __global__ void __launch_bounds__(kAppThreads, 2)
           x[4 * q] += v.x; x[4 * q + 1] += v.y; x[4 * q + 2] += v.z; x[4 * q + 3] += v.w;
         }
       }
-      to_consecutive(x, lane);
       const Tok t = token(ents[r0 + warp]);
       rotate_row(x, p, theta, t.pos + 1 + p.lookahead - p.window - p.stride, lane);
       store_row<FMT>(x, lane, t.slot, p.comp_codes, p.comp_scales);
@@ -604,7 +640,6 @@ __global__ void __launch_bounds__(kAppThreads) append_rows_kernel(const __grid_c
     float x[kPer];
     unpack8(v0, x);
     unpack8(v1, x + 8);
-    to_consecutive(x, lane);
     rotate_row(x, p, theta, int(at), lane);
     store_row<FMT>(x, lane, slot, p.win_codes, p.win_scales);
   }
