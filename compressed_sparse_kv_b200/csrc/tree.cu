@@ -70,6 +70,7 @@ constexpr int kVBytes = 2 * kVPart;     // 64 KB
 constexpr int kPBytes = 2 * kQ * 128;   // weights: 2 chunks of 64 rows
 constexpr int kMaxBatch = 1024;
 constexpr int kMaxNodes = 256;
+constexpr int kRot = 256;       // output rotations kept per group (64 channels: of 8 nodes); others are formed per query
 constexpr int kKey0 = 2, kKeyWarps = 4, kVal0 = kKey0 + kKeyWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;    // O: 2 x 128 columns
@@ -84,21 +85,21 @@ constexpr int kSplitCost = 3;
 // out again, which needs a normal reciprocal.  Such a row's values are below 2^-91.
 constexpr float kMinScale = 0x1p-100f;
 
-// Warps: 0 schedule and queries, 1 products, 2-5 keys, then the value loaders, then the softmax and epilogue.  bf16
-// rows need few loader threads (TMA, cp.async) and 16 softmax warps; quantised rows are converted by 8 loader warps,
-// and 8 softmax warps leave them the registers for 8 loads of 16 bytes in flight each.
+constexpr int kValWarps = 4, kValRows = kRows / kValWarps;  // (a lane looks up one row)
+constexpr int kSoft0 = kVal0 + kValWarps, kSoftWarps = 8;
+constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kSoft0 + kSoftWarps);
+constexpr int kCols = 32;    // rows of a tile per softmax thread: two warps share a quarter of the TMEM lanes
+constexpr int kChans = 128;  // output channels per softmax thread
+
+// Warps: 0 schedule and queries, 1 products, 2-5 keys, 6-9 values, then 8 for the softmax and epilogue.  (16 softmax
+// warps leave 72 registers a thread: 241 against 223 us for long dense contexts in bf16, and quantised rows want the
+// registers for 8 loads of 16 bytes in flight; 2 value warps: 56 against 53 us for selected rows.)
 template <int FMT>
 struct Cfg {
   static constexpr bool kQuant = FMT != DSV4KV_BF16;
   static constexpr bool kRowScale = FMT == DSV4KV_FP8_E4M3_ROW || FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16;
   static constexpr uint32_t kIdescQK = kQuant ? idesc_f16(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
   static constexpr uint32_t kIdescPV = kQuant ? idesc_f16(128, 256, 0, 1) : idesc_bf16(128, 256, 0, 1);
-  static constexpr int kValWarps = kQuant ? 4 : 2, kValRows = kRows / kValWarps;
-  static constexpr int kSoft0 = kVal0 + kValWarps, kSoftWarps = kQuant ? 8 : 16;
-  static constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kSoft0 + kSoftWarps);
-  static constexpr int kGroups = kSoftWarps / 4;  // softmax warps that share a quarter of the TMEM lanes
-  static constexpr int kCols = 64 / kGroups;      // rows of a tile per softmax thread
-  static constexpr int kChans = 256 / kGroups;    // output channels per softmax thread
 };
 
 // A cut group's run of tiles in one pair; slot 2c: the run does not start the group, 2c + 1: it starts it.
@@ -165,6 +166,7 @@ struct __align__(16) Ctl {
   uint8_t row_node[kQ];     // and its number within the CTA's
   uint32_t anc[kQ][kMaxNodes / 32];
   int16_t parent[kMaxNodes];
+  float2 rot[kRot];         // rotations of the CTA's nodes' outputs, where they fit
   int gpre[kMaxBatch + 1];  // groups before sequence b
 };
 
@@ -207,20 +209,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   if (lane == 0) ok = wait_bar(bar, parity, abort);
   return __shfl_sync(kFull, ok, 0);
 }
-template <int N>
-__device__ __forceinline__ bool soft_or(bool pred) {  // over the N softmax threads
+__device__ __forceinline__ bool soft_or(bool pred) {  // over the softmax threads
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.cta.red.or.pred po, 1, %2, pi;\n\tselp.u32 "
       "%0, 1, 0, po;\n\t}"
       : "=r"(r)
-      : "r"(uint32_t(pred)), "n"(N)
+      : "r"(uint32_t(pred)), "n"(kSoftThreads)
       : "memory");
   return r != 0;
 }
-template <int N>
 __device__ __forceinline__ void soft_sync() {
-  asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {  // max relative error ~2^-22, far below the weights' 16 bits
@@ -228,9 +228,6 @@ __device__ __forceinline__ float exp2_approx(float x) {  // max relative error ~
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
 
 __device__ __noinline__ void rotation(double theta_pi, int pos, float* cs, float* sn) {
   rope_rotation(theta_pi, -double(pos), cs, sn);
@@ -440,11 +437,10 @@ __device__ __noinline__ void zero_bad_row(uint8_t* sV, int r) {
 
 // ---------------------------------------------------------------- the kernel
 template <int FMT>
-__global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_comp,
                 const __grid_constant__ Params p) {
   using C = Cfg<FMT>;
-  constexpr int kSoftThreads = C::kSoftThreads, kCols = C::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -459,15 +455,15 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
   pdl_trigger();
 
   if (tid == 0) {
-    mbar_init(&ctl->q_ready, C::kQuant ? 2 * C::kSoftWarps : 1);
+    mbar_init(&ctl->q_ready, C::kQuant ? 2 * kSoftWarps : 1);
     mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->meta, C::kSoftWarps);
+    mbar_init(&ctl->meta, kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctl->k_full[x], 2 * kKeyWarps);
-      mbar_init(&ctl->v_full[x], C::kValWarps);
-      mbar_init(&ctl->p_full[x], C::kSoftWarps);
-      mbar_init(&ctl->info[x], C::kValWarps);
-      mbar_init(&ctl->v_here[x], C::kValWarps / 2);
+      mbar_init(&ctl->v_full[x], kValWarps);
+      mbar_init(&ctl->p_full[x], kSoftWarps);
+      mbar_init(&ctl->info[x], kValWarps);
+      mbar_init(&ctl->v_here[x], kValWarps / 2);
       mbar_init(&ctl->s_full[x], 1);
       mbar_init(&ctl->k_empty[x], 1);
       mbar_init(&ctl->v_empty[x], 1);
@@ -489,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
 
   // ---- the batch: groups and tiles of every sequence (in the weights' place), then which part is this pair's
   int* tiles = reinterpret_cast<int*>(sP);
-  for (int b = tid; b < p.batch; b += C::kThreads) {
+  for (int b = tid; b < p.batch; b += kThreads) {
     int c0, m;
     uint32_t* st = blockIdx.x == 0 ? p.status : nullptr;
     seq_nodes(p, b, &c0, &m, st);
@@ -671,14 +667,14 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         if (!ok) wait_drain(&ctl->o_done, segs & 1);
       }
     }
-  } else if (warp >= C::kSoft0) {
+  } else if (warp >= kSoft0) {
     // ------------------------------------------------------------ softmax, epilogue
     // TMEM lane 64 h + j: query j against rows 64 h + .. (scores), channels 256 h + .. (output)
-    const int wq = warp & 3, cg = (warp - C::kSoft0) >> 2, h = wq >> 1;
+    const int wq = warp & 3, cg = (warp - kSoft0) >> 2, h = wq >> 1;
     const int j = 32 * (wq & 1) + lane;            // this thread's query
     const int r0 = 64 * h + kCols * cg;            // its first row of a tile
     const uint32_t lane_base = uint32_t(32 * wq) << 16;
-    const int q = tid - 32 * C::kSoft0;  // (q < 64) the query that this thread keeps the statistics of
+    const int q = tid - 32 * kSoft0;  // (q < 64) the query that this thread keeps the statistics of
     bool dead = false;  // after a wait gave up: skips every access, still takes part in the group's barriers
     while (next_part()) {
       load_part();
@@ -716,7 +712,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         ctl->row_pos[q] = -1;
       }
       if (q == kQ) ctl->p_max = 0;
-      soft_sync<kSoftThreads>();
+      soft_sync();
       for (int i = first + q; i <= last; i += kSoftThreads) {
         int d = 0;
         const int gj = i - node0;
@@ -736,7 +732,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           }
         }
       }
-      soft_sync<kSoftThreads>();
+      soft_sync();
       if (lane == 0) mbar_arrive(&ctl->meta);
       const bool live = j < rows;
       const int pos = ctl->row_pos[j];
@@ -757,17 +753,26 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           if (lane == 0) mbar_arrive_pair(lead_addr(&ctl->q_ready));
         }
       }
+      // the rotations of the CTA's nodes, while the first tiles are on their way
+      const bool final_out = s.t0 == 0 && s.t1 == s.tiles;
+      const int pairs = p.rope_dim / 2;
+      const bool table = n_nodes * pairs <= kRot;
+      if (final_out && table)
+        for (int x = q; x < n_nodes * pairs; x += kSoftThreads) {
+          const int node = x / pairs, at = p.idx ? 0 : max(0, (node0 + node) * p.heads - f);  // its first query row here
+          rotation(p.rope.theta_pi[x - node * pairs], ctl->row_pos[at], &ctl->rot[x].x, &ctl->rot[x].y);
+        }
       float l = 0.f;
 #pragma unroll 1
       for (int i = 0; i < nt; ++i) {
         const int T = s.t0 + i, c = cnt + i, sb = c & 1;
         if (!dead) dead = !warp_wait(&ctl->info[sb], (c >> 1) & 1, abort, lane);
         bool plain = true;
-        uint32_t seen = live ? (kCols == 32 ? kFull : (1u << (kCols & 31)) - 1u) : 0u;
+        uint32_t seen = live ? kFull : 0u;
         if (!dead) {
           uint32_t pl = kFull;
 #pragma unroll
-          for (int x = 0; x < C::kValWarps; ++x) pl &= ctl->plain[sb][x];
+          for (int x = 0; x < kValWarps; ++x) pl &= ctl->plain[sb][x];
           plain = pl == kFull;
           if (!plain && live) {
             // compressed and window rows by position, drafted ones (consecutive) by the node's ancestor bits
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
               const int w = max(d0, 0) >> 5;
               uint32_t bits = __funnelshift_r(anc[w], w + 1 < kMaxNodes / 32 ? anc[w + 1] : 0u, max(d0, 0) & 31);
               if (d0 < 0) bits <<= -d0;
-              seen |= kCols == 32 ? bits : bits & ((1u << (kCols & 31)) - 1u);
+              seen |= bits;
             }
           }
         }
@@ -797,7 +802,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           if (!dead) {
             tc_fence_after();
             uint32_t raw[kCols];
-            tmem_ld_cols(tmem + lane_base + kColS + 64 * sb + kCols * cg, raw);
+            tmem_ld32(tmem + lane_base + kColS + 64 * sb + kCols * cg, raw);
             tmem_wait_ld();
             const float m = ctl->m[j];
             if (!plain && again == 0 && T >= s.full) {
@@ -821,19 +826,19 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kCols; ++x) d[x] -= m;
           }
-          if (again || !soft_or<kSoftThreads>(raise)) break;
+          if (again || !soft_or(raise)) break;
           ctl->part[2 * cg + h][j] = top;
-          soft_sync<kSoftThreads>();
+          soft_sync();
           if (q < kQ) {
             float mx = ctl->part[0][q];
 #pragma unroll
-            for (int x = 1; x < 2 * C::kGroups; ++x) mx = fmaxf(mx, ctl->part[x][q]);
+            for (int x = 1; x < 4; ++x) mx = fmaxf(mx, ctl->part[x][q]);
             const float m = ctl->m[q];
             const bool up = mx > m + kRaise;
             ctl->alpha[q] = up ? exp2_approx(m - mx) : 1.f;
             if (up) ctl->m[q] = mx;
           }
-          soft_sync<kSoftThreads>();
+          soft_sync();
           const float a = ctl->alpha[j];
           l *= a;
           if (i > 0) {  // the accumulator too, once the products before this tile's are in
@@ -841,9 +846,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
             if (!dead) {
               tc_fence_after();
 #pragma unroll 1
-              for (int x = 0; x < C::kChans; x += 16) {
+              for (int x = 0; x < kChans; x += 16) {
                 uint32_t o[16];
-                const uint32_t addr = tmem + lane_base + kColO + C::kChans * cg + x;
+                const uint32_t addr = tmem + lane_base + kColO + kChans * cg + x;
                 tmem_ld16(addr, o);
                 tmem_wait_ld();
 #pragma unroll
@@ -884,28 +889,16 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         if (lane == 0) mbar_arrive_pair(lead_addr(&ctl->p_full[h]));
       }
       // ---- epilogue
-      soft_sync<kSoftThreads>();  // (part is free: the last raise has been read)
+      soft_sync();  // (part is free: the last raise has been read)
       ctl->part[2 * cg + h][j] = l;
-      if (!dead) dead = !warp_wait(&ctl->o_done, segs & 1, abort, lane);
-      tc_fence_after();
-      // the rotations of the CTA's nodes, in the weights' place (the products have read them)
-      const bool final_out = s.t0 == 0 && s.t1 == s.tiles;
-      const int pairs = p.rope_dim / 2;
-      float2* rot = reinterpret_cast<float2*>(sP);
-      const bool table = n_nodes * pairs <= kPBytes / 8;
-      if (!dead && final_out && table)
-        for (int x = q; x < n_nodes * pairs; x += kSoftThreads) {
-          const int node = x / pairs, at = p.idx ? 0 : max(0, (node0 + node) * p.heads - f);  // its first query row here
-          rotation(p.rope.theta_pi[x - node * pairs], ctl->row_pos[at], &rot[x].x, &rot[x].y);
-        }
-      soft_sync<kSoftThreads>();
+      soft_sync();
       const int slot = 2 * pair + (s.t0 == 0 ? 1 : 0);
-      if (!dead && q < kQ) {
+      if (q < kQ) {
         float L = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2 * C::kGroups; ++x) L += ctl->part[x][q];
+        for (int x = 0; x < 4; ++x) L += ctl->part[x][q];
         ctl->alpha[q] = !final_out ? 1.f : L == 0.f ? 0.f : __frcp_rn(L);  // (no row: zeros)
-        if (!final_out) {
+        if (!final_out && !dead) {
           // (a query that is not finite: its NaN has to pass the merge, which skips runs without rows)
           p.ml[size_t(slot) * kGroup + rank * kQ + q] =
               make_float4(L != L ? INFINITY : ctl->m[q], L, __int_as_float(ctl->row_pos[q]),
@@ -913,18 +906,20 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
           if (q == 0 && rank == 0) p.rec[slot] = Rec{1, s.b, s.g, s.t0, s.t1, s.tiles, 0, 0};
         }
       }
-      soft_sync<kSoftThreads>();
+      soft_sync();
+      if (!dead) dead = !warp_wait(&ctl->o_done, segs & 1, abort, lane);
+      tc_fence_after();
       if (!dead) {
         const float a = ctl->alpha[j];
-        const float2* my_rot = rot + ctl->row_node[j] * pairs;
+        const float2* my_rot = ctl->rot + ctl->row_node[j] * pairs;
         const int rch = kDim - p.rope_dim, odd = lane & 1;
         // lane pairs swap 16-byte pieces, so that a store fills whole 32-byte sectors: first the even lane's row
         const bool live_e = (j & ~1) < rows, live_o = (j | 1) < rows;
 #pragma unroll 1
-        for (int x = 0; x < C::kChans; x += 16) {
-          const int ch = kHalf * h + C::kChans * cg + x;
+        for (int x = 0; x < kChans; x += 16) {
+          const int ch = kHalf * h + kChans * cg + x;
           uint32_t o[16];
-          tmem_ld16(tmem + lane_base + kColO + C::kChans * cg + x, o);
+          tmem_ld16(tmem + lane_base + kColO + kChans * cg + x, o);
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 16; ++y) o[y] = a == 0.f ? 0u : __float_as_uint(__uint_as_float(o[y]) * a);
@@ -972,19 +967,18 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         }
       }
       tc_fence_before();
-      soft_sync<kSoftThreads>();  // (the statistics and rotations are read; the next part overwrites them)
+      soft_sync();  // (the statistics and rotations are read; the next part overwrites them)
     }
   } else if (warp >= kVal0) {
     // ------------------------------------------------------------ values, and what the rows are
-    const int vw = warp - kVal0, half = vw / (C::kValWarps / 2);
-    constexpr int kX = C::kValRows / 32;  // rows a lane
-    // tile T's rows of this warp: the one TMA row, or kX rows a lane
+    const int vw = warp - kVal0, half = vw / (kValWarps / 2);
+    // tile T's rows of this warp: the one TMA row, or a row a lane
     struct Set {
       bool tma;
       int32_t row0;
-      const uint8_t *my[kX], *mysc[kX];
-      float sr[kX];
-      Key key[kX];
+      const uint8_t *my, *mysc;
+      float sr;
+      Key key;
     };
     int last_met = -1;  // the last part whose nodes were waited for
     bool ok = true;
@@ -1000,19 +994,16 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       e.tma = !C::kQuant && T < s.full && tma_rows(p, s.b, T, trow);
       e.row0 = half ? trow[1] : trow[0];
       if (e.tma) return;
-#pragma unroll
-      for (int x = 0; x < kX; ++x) {
-        int64_t row;
-        const Rows* src = row_source(p, s, ctl, T, C::kValRows * vw + 32 * x + lane, &row, &e.key[x], met);
-        e.my[x] = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
-        if (FMT == DSV4KV_FP4_E2M1_G16)
-          e.mysc[x] = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
-        if (C::kRowScale) {
-          e.sr[x] = src ? static_cast<const float*>(src->scales)[row] : 1.f;
-          if (e.sr[x] == 0.f) {  // a row of zeros
-            e.sr[x] = 1.f;
-            e.my[x] = nullptr;
-          }
+      int64_t row;
+      const Rows* src = row_source(p, s, ctl, T, kValRows * vw + lane, &row, &e.key, met);
+      e.my = src ? src->codes + size_t(row) * row_bytes(FMT) : nullptr;
+      if (FMT == DSV4KV_FP4_E2M1_G16)
+        e.mysc = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
+      if (C::kRowScale) {
+        e.sr = src ? static_cast<const float*>(src->scales)[row] : 1.f;
+        if (e.sr == 0.f) {  // a row of zeros
+          e.sr = 1.f;
+          e.my = nullptr;
         }
       }
     };
@@ -1023,7 +1014,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
       Dequant<C::kQuant ? FMT : DSV4KV_FP8_E4M3_ROW, 32> dq;
       resolve(cur, s.t0);
       if (!ok) break;
-      if constexpr (C::kQuant) dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, 0, lane);
+      if constexpr (C::kQuant) dq.fetch(cur.my, cur.mysc, kHalf * rank, 0, lane);
 #pragma unroll 1
       for (int i = 0; i < nt && ok; ++i) {
         const int T = s.t0 + i, c = cnt + i, sb = c & 1;
@@ -1032,31 +1023,28 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         if (cur.tma) {
           if (lane == 0) ctl->plain[sb][vw] = kFull;
         } else {
-          uint32_t plain = kFull;
-#pragma unroll
-          for (int x = 0; x < kX; ++x) {
-            const int r = C::kValRows * vw + 32 * x + lane;
-            if (C::kRowScale) {
-              const float sr = cur.sr[x], at_least = fmaxf(sr, kMinScale);
-              inv = 1.f / at_least;
-              ctl->scale[sb][r] = sr;
-              ctl->lscale[sb][r] = __log2f(at_least);
-              ctl->iscale[sb][r] = inv;
-            }
-            ctl->key[sb][r] = cur.key[x];
-            plain &= __ballot_sync(kFull, cur.key[x].lo == 0 && cur.key[x].hi == kNever);
+          const int r = kValRows * vw + lane;
+          if (C::kRowScale) {
+            const float sr = cur.sr, at_least = fmaxf(sr, kMinScale);
+            inv = 1.f / at_least;
+            ctl->scale[sb][r] = sr;
+            ctl->lscale[sb][r] = __log2f(at_least);
+            ctl->iscale[sb][r] = inv;
           }
+          ctl->key[sb][r] = cur.key;
+          const uint32_t plain = __ballot_sync(kFull, cur.key.lo == 0 && cur.key.hi == kNever);
           if (lane == 0) ctl->plain[sb][vw] = plain;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->info[sb]);
-        if (i + 1 < nt) resolve(nxt, T + 1);  // (its table and index reads, while the buffer is in use)
+        // the next tile's table and index reads: while this one's buffer is in use, or (below) its copies run
+        if ((C::kQuant || cur.tma) && i + 1 < nt) resolve(nxt, T + 1);
         if (ok && c > 0) ok = warp_wait(&ctl->v_empty[half], (c - 1) & 1, abort, lane);
         if (!ok) break;
         const uint32_t bar = lead_addr(&ctl->v_full[half]);
         if (cur.tma) {
           if (lane == 0) {
-            const bool mine = vw % (C::kValWarps / 2) == 0;  // one warp a half
+            const bool mine = vw % (kValWarps / 2) == 0;  // one warp a half
             if (mine && rank == 0) mbar_arrive_expect_tx(&ctl->v_full[half], 2 * kVPart);
             else mbar_arrive_pair(bar);
             if (mine) tma_load_3d_pair(sV + half * kVPart, &tm_comp, bar, 0, cur.row0, 4 * rank);
@@ -1066,23 +1054,25 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         } else {
           if constexpr (C::kQuant) {
             const int nb = dq.batches(kHalf * rank);
-            auto cell = [&](int r, int ch) { return val_cell(sV, C::kValRows * vw + r, ch); };
+            auto cell = [&](int r, int ch) { return val_cell(sV, kValRows * vw + r, ch); };
             dq.put(inv, kHalf * rank, 0, lane, cell);
 #pragma unroll 1
             for (int x = 1; x < nb; ++x) {
-              dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, x, lane);
+              dq.fetch(cur.my, cur.mysc, kHalf * rank, x, lane);
               dq.put(inv, kHalf * rank, x, lane, cell);
             }
           } else {
+            // 8 lanes a row, 4 rows at a time: 64 channels (a slab) of each, slab after slab
+#pragma unroll 4
+            for (int r = lane >> 3; r < 32; r += 4) {
+              const uint8_t* g = shfl_ptr(cur.my, r);
+              uint8_t* dst = val_cell(sV, kValRows * vw + r, 8 * (lane & 7));
+              const uint8_t* src = g ? g + 2 * kHalf * rank + 16 * (lane & 7) : p.draft.codes;
 #pragma unroll
-            for (int x = 0; x < kX; ++x)
-#pragma unroll 8
-              for (int r = 0; r < 32; ++r) {  // a row's 256 channels: 32 lanes of 16 bytes
-                const uint8_t* g = shfl_ptr(cur.my[x], r);
-                cp_async16_zfill(val_cell(sV, C::kValRows * vw + 32 * x + r, 8 * lane),
-                                 g ? g + 2 * (kHalf * rank + 8 * lane) : p.draft.codes, g ? 16 : 0);
-              }
+              for (int y = 0; y < 4; ++y) cp_async16_zfill(dst + y * kVSlab, src + (g ? 128 * y : 0), g ? 16 : 0);
+            }
             cp_async_commit();
+            if (i + 1 < nt) resolve(nxt, T + 1);
             cp_async_wait_group<0>();
           }
           fence_proxy_async_smem();
@@ -1094,7 +1084,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
         }
         cur = nxt;
         if constexpr (C::kQuant)
-          if (i + 1 < nt) dq.fetch(cur.my[0], cur.mysc[0], kHalf * rank, 0, lane);
+          if (i + 1 < nt) dq.fetch(cur.my, cur.mysc, kHalf * rank, 0, lane);
       }
     }
   } else {
@@ -1143,7 +1133,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < nt && ok; ++i) {
         const int T = s.t0 + i, c = cnt + i;
-        if (i + 1 < nt) resolve(nxt, T + 1);  // (its table and index reads, while the buffer is in use)
+        if ((C::kQuant || cur.tma) && i + 1 < nt) resolve(nxt, T + 1);  // (as the values')
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
           if (c > 0) ok = warp_wait(&ctl->k_empty[x], (c - 1) & 1, abort, lane);
@@ -1159,11 +1149,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
             continue;
           }
           if constexpr (!C::kQuant) {
-#pragma unroll 8
-            for (int r = 0; r < 16; ++r) {  // a row's 256 channels: 32 lanes of 16 bytes
+#pragma unroll
+            for (int r = lane >> 3; r < 16; r += 4) {  // as the values
               const uint8_t* g = shfl_ptr(cur.my, r);
-              const int ch = kHalf * x + 8 * lane;
-              cp_async16_zfill(key_cell(sK, 16 * kw + r, ch), g ? g + 2 * ch : p.draft.codes, g ? 16 : 0);
+              uint8_t* dst = key_cell(sK, 16 * kw + r, kHalf * x + 8 * (lane & 7));
+              const uint8_t* src = g ? g + 2 * kHalf * x + 16 * (lane & 7) : p.draft.codes;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) cp_async16_zfill(dst + y * kKSlab, src + (g ? 128 * y : 0), g ? 16 : 0);
             }
             cp_async_commit();
             if (x == 0) continue;  // (handed over below, while the second half is on its way)
@@ -1171,6 +1163,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(lead_addr(&ctl->k_full[0]));
+            if (i + 1 < nt) resolve(nxt, T + 1);
             cp_async_wait_group<0>();
           } else {
             auto cell = [&](int r, int ch) { return key_cell(sK, 16 * kw + r, kHalf * x + ch); };
@@ -1308,7 +1301,7 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tc, const Para
     if (e != cudaSuccess) return e;
     mark_done_on_device(ready);
   }
-  return launch_pdl_cluster(tree_kernel<FMT>, dim3(unsigned(2 * P)), dim3(Cfg<FMT>::kThreads), kSmemBytes, 2, stream, tq, tc,
+  return launch_pdl_cluster(tree_kernel<FMT>, dim3(unsigned(2 * P)), dim3(kThreads), kSmemBytes, 2, stream, tq, tc,
                             p);
 }
 
