@@ -364,10 +364,14 @@ struct Dequant {
 
   __device__ __forceinline__ void fetch(const uint8_t* my, const uint8_t* mysc, int ch0, int batch, int lane) {
     const int bd = body(ch0), upr = per_row(ch0);
+    // (first all rows' addresses: a shuffle's and then a load's wait for the queue they share would come 8 times over)
+    const uint8_t* rows[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) rows[i] = shfl_ptr(my, min((32 * (kN * batch + i) + lane) / upr, kR - 1));
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int x = 32 * (kN * batch + i) + lane, r = x / upr, u = x - r * upr;
-      const uint8_t* row = shfl_ptr(my, min(r, kR - 1));
+      const uint8_t* row = rows[i];
       const bool in = r < kR && row;
       raw[i] = in ? ld_stream_v4(row + (kFp4 ? ch0 / 2 + 16 * u : kRope && u >= bd ? kDim - 64 + 16 * (u - bd) : ch0 + 16 * u))
                   : make_uint4(0, 0, 0, 0);
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ Params p) {
   using C = Cfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (an offset: the accesses stay shared-memory ones)
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + kQBytes;
   uint8_t* sV = sK + kKBytes;
@@ -1063,9 +1067,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
             // 8 lanes a row, 4 rows at a time: 64 channels (a slab) of each, slab after slab
-#pragma unroll 4
-            for (int r = lane >> 3; r < 32; r += 4) {
-              const uint8_t* g = shfl_ptr(cur.my, r);
+            const uint8_t* rows[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) rows[y] = shfl_ptr(cur.my, (lane >> 3) + 4 * y);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const int r = (lane >> 3) + 4 * z;
+              const uint8_t* g = rows[z];
               uint8_t* dst = val_cell(sV, kValRows * vw + r, 8 * (lane & 7));
               const uint8_t* src = g ? g + 2 * kHalf * rank + 16 * (lane & 7) : p.draft.codes;
 #pragma unroll
@@ -1122,6 +1130,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sr == 0.f) e.my = nullptr;  // a row of zeros
       }
     };
+    // the rows of a tile on their way to L2 (the keys' and the values' loads come after): two lanes a row
+    auto ahead = [&](const Set& e) {
+      constexpr int kBytes = row_bytes(FMT) / 2;
+      if (e.my)
+#pragma unroll
+        for (int x = 0; x < kBytes; x += 128) prefetch_l2(e.my + kBytes * (lane >> 4) + x);
+    };
     while (ok && next_part()) {
       load_part();
       const int nt = s.t1 - s.t0;
@@ -1133,7 +1148,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < nt && ok; ++i) {
         const int T = s.t0 + i, c = cnt + i;
-        if ((C::kQuant || cur.tma) && i + 1 < nt) resolve(nxt, T + 1);  // (as the values')
+        if ((C::kQuant || cur.tma) && i + 1 < nt) {  // (as the values')
+          resolve(nxt, T + 1);
+          if (C::kQuant) ahead(nxt);
+        }
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
           if (c > 0) ok = warp_wait(&ctl->k_empty[x], (c - 1) & 1, abort, lane);
@@ -1149,9 +1167,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           if constexpr (!C::kQuant) {
+            const uint8_t* rows[4];  // as the values
 #pragma unroll
-            for (int r = lane >> 3; r < 16; r += 4) {  // as the values
-              const uint8_t* g = shfl_ptr(cur.my, r);
+            for (int z = 0; z < 4; ++z) rows[z] = shfl_ptr(cur.my, (lane >> 3) + 4 * z);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int r = (lane >> 3) + 4 * z;
+              const uint8_t* g = rows[z];
               uint8_t* dst = key_cell(sK, 16 * kw + r, kHalf * x + 8 * (lane & 7));
               const uint8_t* src = g ? g + 2 * kHalf * x + 16 * (lane & 7) : p.draft.codes;
 #pragma unroll
@@ -1175,11 +1197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               dq.put(cur.inv, kHalf * x, y, lane, cell);
             }
           }
+          if constexpr (C::kQuant)
+            if (x == 0) dq.fetch(cur.my, cur.mysc, kHalf, 0, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive_pair(bar);
-          if constexpr (C::kQuant)
-            if (x == 0) dq.fetch(cur.my, cur.mysc, kHalf, 0, lane);
         }
         if (!ok) cp_async_wait_group<0>();
         cur = nxt;
