@@ -266,9 +266,7 @@ constexpr int kAppWarps = 8;
 constexpr int kAppThreads = 32 * kAppWarps;
 constexpr int kD = 512, kPer = kD / 32;
 constexpr int kMaxTokens = 512;  // tokens a CTA
-constexpr int kGroup = 2;        // long entries summed together
-constexpr int kAhead = 4;        // taps of them that a warp has in flight
-constexpr int kLongTaps = 32;    // entries of more taps are summed by the whole CTA
+constexpr int kLongTaps = 32;    // entries of more taps are summed by a cluster
 
 enum : int { kPartEntries = 1, kPartWindow = 2, kPartRing = 4 };
 
@@ -401,12 +399,16 @@ __device__ __forceinline__ void sums_of(const uint64_t (&acc)[kPer / 2], float (
   }
 }
 
-// Appends i to list[n ..] where `keep`, in thread order; returns the new length.  All threads call it.
+__device__ __forceinline__ void app_sync() {  // the 8 working warps (a long entry's CTA has a ninth)
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kAppThreads) : "memory");
+}
+
+// Appends i to list[n ..] where `keep`, in thread order; returns the new length.  The 8 working warps call it.
 __device__ __forceinline__ int push_ordered(bool keep, int i, int32_t* list, int n, int* wcnt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned m = __ballot_sync(kFull, keep);
   if (lane == 0) wcnt[warp] = __popc(m);
-  __syncthreads();
+  app_sync();
   int before = n, all = n;
 #pragma unroll
   for (int k = 0; k < kAppWarps; ++k) {
@@ -414,28 +416,20 @@ __device__ __forceinline__ int push_ordered(bool keep, int i, int32_t* list, int
     all += wcnt[k];
   }
   if (keep) list[before + __popc(m & ((1u << lane) - 1u))] = i;
-  __syncthreads();
+  app_sync();
   return all;
 }
 
-template <int FMT, bool kLong>
-__global__ void __launch_bounds__(kAppThreads, 2)
-    append_paged_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ int32_t rows[kMaxTokens], ents[kMaxTokens];
-  __shared__ int wcnt[kAppWarps];
-  extern __shared__ __align__(16) float red[];  // long entries: [warp][group][512]; short ones: the weights
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i_first = blockIdx.x * p.per, i_end = min(p.tokens, i_first + p.per);
-  const int R = p.window + p.k_taps;
-  const double theta = p.rope.theta_pi[lane];
-  pdl_trigger();
-  pdl_wait();
-  // a token of a list
-  auto token = [&](int i) {
-    const int b = __ldg(p.seq + i);
-    const int pos = int(__ldg(p.pos + i)), slot = __ldg(p.comp_slot + i);
-    return Tok{i, b, pos, __ldg(p.cu + b), slot};
-  };
+// A token of a list.
+__device__ __forceinline__ Tok token(const AppendParams& p, int i) {
+  const int b = __ldg(p.seq + i);
+  const int pos = int(__ldg(p.pos + i)), slot = __ldg(p.comp_slot + i);
+  return Tok{i, b, pos, __ldg(p.cu + b), slot};
+}
+
+// Lists the CTA's tokens whose row stays and those that emit an entry, in order; (rows, entries) counted.
+__device__ __forceinline__ int2 list_tokens(const AppendParams& p, int32_t* rows, int32_t* ents, int* wcnt) {
+  const int i_first = int(blockIdx.x) * p.per, i_end = min(p.tokens, i_first + p.per), R = p.window + p.k_taps;
   int n_rows = 0, n_ents = 0;
   for (int i0 = i_first; i0 < i_end; i0 += kAppThreads) {
     const int i = i0 + int(threadIdx.x);
@@ -464,9 +458,15 @@ __global__ void __launch_bounds__(kAppThreads, 2)
     n_rows = push_ordered(row, i, rows, n_rows, wcnt);
     n_ents = push_ordered(ent, i, ents, n_ents, wcnt);
   }
-  // ring and window rows
+  return make_int2(n_rows, n_ents);
+}
+
+// Ring and window rows of the listed tokens, one warp a row.
+template <int FMT>
+__device__ __forceinline__ void write_rows(const AppendParams& p, const int32_t* rows, int n_rows, double theta) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = p.window + p.k_taps;
   for (int r = warp; r < n_rows; r += kAppWarps) {
-    const Tok k = token(rows[r]);
+    const Tok k = token(p, rows[r]);
     const uint16_t* src = p.s_new + size_t(k.i) * kD + 8 * lane;
     const uint4 v0 = first_piece(src), v1 = second_piece(src);
     if ((p.parts & kPartRing) && p.cu[k.b + 1] - 1 - k.i < R) {
@@ -483,136 +483,263 @@ __global__ void __launch_bounds__(kAppThreads, 2)
       store_row<FMT>(x, lane, slot, p.win_codes, p.win_scales);
     }
   }
-  if constexpr (!kLong) {
-    if (n_ents == 0) return;
-    // weights [tap][quarter][lane] float4: a lane's two pieces of 8 channels in four conflict-free reads
-    ulonglong2* sw = reinterpret_cast<ulonglong2*>(red);
-    for (int i = threadIdx.x; i < p.k_taps * (kD / 4); i += kAppThreads) {
-      const int j = i / (kD / 4), c = i % (kD / 4);  // quad c: lane (c / 2) % 32, quarter 2 (c / 64) + c % 2
-      sw[(j * 4 + 2 * (c >> 6) + (c & 1)) * 32 + ((c >> 1) & 31)] = reinterpret_cast<const ulonglong2*>(p.w)[i];
-    }
-    __syncthreads();
-    // consecutive entries to one warp: the rows that two entries share come from L1 the second time
-    const int per = (n_ents + kAppWarps - 1) / kAppWarps, end = min(n_ents, (warp + 1) * per);
-    Tok next = warp * per < end ? token(ents[warp * per]) : Tok{};
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kAppThreads, 2) append_paged_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ int32_t rows[kMaxTokens], ents[kMaxTokens];
+  __shared__ int wcnt[kAppWarps];
+  extern __shared__ __align__(16) float weights[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const double theta = p.rope.theta_pi[lane];
+  pdl_trigger();
+  pdl_wait();
+  const int2 n = list_tokens(p, rows, ents, wcnt);
+  const int n_ents = n.y;
+  write_rows<FMT>(p, rows, n.x, theta);
+  if (n_ents == 0) return;
+  // weights [tap][quarter][lane] float4: a lane's two pieces of 8 channels in four conflict-free reads
+  ulonglong2* sw = reinterpret_cast<ulonglong2*>(weights);
+  for (int i = threadIdx.x; i < p.k_taps * (kD / 4); i += kAppThreads) {
+    const int j = i / (kD / 4), c = i % (kD / 4);  // quad c: lane (c / 2) % 32, quarter 2 (c / 64) + c % 2
+    sw[(j * 4 + 2 * (c >> 6) + (c & 1)) * 32 + ((c >> 1) & 31)] = reinterpret_cast<const ulonglong2*>(p.w)[i];
+  }
+  __syncthreads();
+  // consecutive entries to one warp: the rows that two entries share come from L1 the second time
+  const int per = (n_ents + kAppWarps - 1) / kAppWarps, end = min(n_ents, (warp + 1) * per);
+  Tok next = warp * per < end ? token(p, ents[warp * per]) : Tok{};
 #pragma unroll 1
-    for (int r = warp * per; r < end; ++r) {
-      const Tok k = next;
-      if (r + 1 < end) next = token(ents[r + 1]);
-      const int q0 = k.pos + 1 + p.lookahead - p.window - p.k_taps;
-      const int i0 = k.i - (k.pos - q0);  // the first tap's token
-      uint64_t acc[kPer / 2];
+  for (int r = warp * per; r < end; ++r) {
+    const Tok k = next;
+    if (r + 1 < end) next = token(p, ents[r + 1]);
+    const int q0 = k.pos + 1 + p.lookahead - p.window - p.k_taps;
+    const int i0 = k.i - (k.pos - q0);  // the first tap's token
+    uint64_t acc[kPer / 2];
 #pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) acc[e] = 0;
-      auto add = [&](int j, const uint4& a, const uint4& b) {
-        const ulonglong2* w = sw + j * 128 + lane;
-        add8(acc, w[0], w[32], a);
-        add8(acc + 4, w[64], w[96], b);
-      };
-      int j0 = max(0, -q0);
-      if (i0 >= k.first) {  // all taps are new tokens: consecutive rows
-        const uint16_t* src = p.s_new + size_t(i0) * kD + 8 * lane;
+    for (int e = 0; e < kPer / 2; ++e) acc[e] = 0;
+    auto add = [&](int j, const uint4& a, const uint4& b) {
+      const ulonglong2* w = sw + j * 128 + lane;
+      add8(acc, w[0], w[32], a);
+      add8(acc + 4, w[64], w[96], b);
+    };
+    int j0 = max(0, -q0);
+    if (i0 >= k.first) {  // all taps are new tokens: consecutive rows
+      const uint16_t* src = p.s_new + size_t(i0) * kD + 8 * lane;
 #pragma unroll 2
-        for (; j0 + 4 <= p.k_taps; j0 += 4) {
-          uint4 a[4], b[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            a[x] = first_piece(src + (j0 + x) * kD);
-            b[x] = second_piece(src + (j0 + x) * kD);
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) add(j0 + x, a[x], b[x]);
-        }
-      }
-#pragma unroll 1
-      for (; j0 < p.k_taps; j0 += 4) {
+      for (; j0 + 4 <= p.k_taps; j0 += 4) {
         uint4 a[4], b[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          if (j0 + x >= p.k_taps) break;
-          const uint16_t* src = state_row(p, k, q0 + j0 + x, lane);
-          a[x] = first_piece(src);
-          b[x] = second_piece(src);
+          a[x] = first_piece(src + (j0 + x) * kD);
+          b[x] = second_piece(src + (j0 + x) * kD);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (j0 + x < p.k_taps) add(j0 + x, a[x], b[x]);
+        for (int x = 0; x < 4; ++x) add(j0 + x, a[x], b[x]);
       }
-      float x[kPer];
-      sums_of(acc, x);
-      rotate_row(x, p, theta, q0 + p.k_taps - p.stride, lane);
-      store_row<FMT>(x, lane, k.slot, p.comp_codes, p.comp_scales);
     }
+#pragma unroll 1
+    for (; j0 < p.k_taps; j0 += 4) {
+      uint4 a[4], b[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (j0 + x >= p.k_taps) break;
+        const uint16_t* src = state_row(p, k, q0 + j0 + x, lane);
+        a[x] = first_piece(src);
+        b[x] = second_piece(src);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (j0 + x < p.k_taps) add(j0 + x, a[x], b[x]);
+    }
+    float x[kPer];
+    sums_of(acc, x);
+    rotate_row(x, p, theta, q0 + p.k_taps - p.stride, lane);
+    store_row<FMT>(x, lane, k.slot, p.comp_codes, p.comp_scales);
+  }
+}
+
+// Long entries: a cluster of 8 CTAs shares the entries of its CTAs' tokens; CTA r has taps [16 r, 16 r + 16) of each (of
+// 128 at a time), whose weights stay in registers: a thread has two channels.
+constexpr int kCl = 8;           // CTAs a cluster
+constexpr int kRound = kCl;      // entries summed before the CTAs exchange their sums: one a CTA to finish
+constexpr int kLongThreads = kAppThreads + 32;
+constexpr int kTaps = 16;        // taps a CTA
+constexpr int kStages = 4;       // entries' rows in flight
+constexpr int kStageBytes = kTaps * kD * 2;
+constexpr int kListed = kAppThreads;  // entries whose tokens are looked up at a time
+constexpr size_t kLongSmem = kStages * kStageBytes + kRound * kD * sizeof(float);
+
+struct LongCtl {
+  uint64_t full[kStages];
+  int n_of[kCl];  // entries of every CTA of the cluster
+  volatile int dead;
+  Tok toks[kListed];
+};
+
+__device__ __forceinline__ bool wait_rows(LongCtl* ctl, int st, uint32_t parity) {  // bounded: one second
+  if (mbar_try_wait(&ctl->full[st], parity)) return true;
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+  while (!ctl->dead) {
+    if (mbar_try_wait(&ctl->full[st], parity)) return true;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    if (t - t0 > 1000000000ull) ctl->dead = 1;
+  }
+  return false;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kLongThreads, 2) append_long_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ int32_t rows[kMaxTokens], ents[kMaxTokens];
+  __shared__ int wcnt[kAppWarps];
+  __shared__ LongCtl ctl;
+  extern __shared__ __align__(128) uint8_t stages[];
+  float* part = reinterpret_cast<float*>(stages + kStages * kStageBytes);  // [CTA][512]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = int(cluster_rank());
+  const double theta = p.rope.theta_pi[lane];
+  const int R = p.window + p.k_taps;
+  const int tp = min(kTaps, (p.k_taps + kCl - 1) / kCl);  // taps a CTA has at a time
+  const int chunks = (p.k_taps + kCl * tp - 1) / (kCl * tp);
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&ctl.full[s], 1);
+    ctl.dead = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  cluster_arrive_relaxed();
+  pdl_wait();
+  int2 n = make_int2(0, 0);
+  if (warp < kAppWarps) n = list_tokens(p, rows, ents, wcnt);
+  __syncwarp();
+  cluster_wait();
+  if (tid < kCl) st_dsmem_u32(dsmem_addr(&ctl.n_of[rank], tid), uint32_t(n.y));
+  __syncwarp();
+  cluster_sync();
+  int total = 0;
+#pragma unroll
+  for (int r = 0; r < kCl; ++r) total += ctl.n_of[r];
+  if (warp == kAppWarps) {
+    // the ninth warp adds up and stores this CTA's entry of every round, while the others sum the next round's
+    for (int x0 = 0, round = 0; x0 < total; x0 += kListed)
+      for (int r0 = 0; r0 < min(kListed, total - x0); r0 += kRound, ++round) {
+        if (round) cluster_wait_acquire_div();
+        cluster_arrive_release_div();
+        cluster_wait_acquire_div();  // every CTA's sums are here
+        if (rank < min(kRound, min(kListed, total - x0) - r0) && !ctl.dead) {
+          float x[kPer];
+#pragma unroll
+          for (int y = 0; y < kPer; ++y) x[y] = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < kCl; ++c)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const float4 v = *reinterpret_cast<const float4*>(part + c * kD + 256 * (h >> 1) + 8 * lane + 4 * (h & 1));
+              x[4 * h] += v.x; x[4 * h + 1] += v.y; x[4 * h + 2] += v.z; x[4 * h + 3] += v.w;
+            }
+          const Tok k = ctl.toks[r0 + rank];
+          rotate_row(x, p, theta, k.pos + 1 + p.lookahead - p.window - p.stride, lane);
+          store_row<FMT>(x, lane, k.slot, p.comp_codes, p.comp_scales);
+        }
+        cluster_arrive_release_div();  // the sums' place is free
+      }
+    if (total) cluster_wait_acquire_div();
     return;
   }
-  if constexpr (kLong) for (int r0 = 0; r0 < n_ents; r0 += kGroup) {
-    const int ng = min(kGroup, n_ents - r0);
-    Tok k[kGroup];
-    int q0[kGroup];
-    uint64_t acc[kGroup][kPer / 2];
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      k[g] = token(ents[min(r0 + g, n_ents - 1)]);
-      q0[g] = k[g].pos + 1 + p.lookahead - p.window - p.k_taps;
-#pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) acc[g][e] = 0;
+  bool rows_done = false;
+  int got = 0, put = 0, round = 0;  // stages consumed, issued (thread 0); rounds of entries
+  uint64_t w[kTaps];
+  for (int base = 0; base < total; base += kListed) {
+    const bool again = base > 0;
+    if (again) cluster_wait_acquire_div();  // (the tokens of the previous entries are read)
+    app_sync();
+    const int listed = min(kListed, total - base);
+    if (tid < listed) {
+      int r = 0, x = base + tid;
+      while (x >= ctl.n_of[r]) x -= ctl.n_of[r++];
+      ctl.toks[tid] = token(p, int(ld_dsmem_u32(dsmem_addr(&ents[x], r))));
     }
-#pragma unroll 1
-    for (int j0 = warp; j0 < p.k_taps; j0 += kAppWarps * kAhead) {
-      uint4 a[kAhead][kGroup], b[kAhead][kGroup];
+    app_sync();
+    // (thread 0) the next slice of an entry's rows: from the raw ring (in two pieces where it wraps) and the new states
+    int ir = 0, ic = 0, ie = 0;  // its round's first entry, chunk, entry within the round
+    auto issue = [&]() {
+      if (ir >= listed || ctl.dead) return;
+      const Tok& k = ctl.toks[ir + ie];
+      const int j0 = kCl * tp * ic + tp * rank;
+      const int q = k.pos + 1 + p.lookahead - p.window - p.k_taps + j0;  // position of the slice's first tap
+      const int lo = min(max(0, -q), tp), hi = max(lo, min(tp, p.k_taps - j0));
+      const int fresh = min(max(k.first - (k.i - k.pos + q), lo), hi);   // first tap that is a new token
+      uint8_t* dst = stages + (put % kStages) * kStageBytes;
+      uint64_t* bar = &ctl.full[put % kStages];
+      mbar_arrive_expect_tx(bar, uint32_t(hi - lo) * kD * 2);
+      if (fresh > lo) {
+        const int r0 = (q + lo) % R, a = min(fresh - lo, R - r0);
+        const uint16_t* ring = p.ring + size_t(k.b) * R * kD;
+        bulk_load_plain(dst + lo * kD * 2, ring + size_t(r0) * kD, uint32_t(a) * kD * 2, bar);
+        if (fresh - lo > a) bulk_load_plain(dst + (lo + a) * kD * 2, ring, uint32_t(fresh - lo - a) * kD * 2, bar);
+      }
+      if (hi > fresh)
+        bulk_load_plain(dst + fresh * kD * 2, p.s_new + size_t(k.i - k.pos + q + fresh) * kD, uint32_t(hi - fresh) * kD * 2,
+                        bar);
+      ++put;
+      if (++ie == min(kRound, listed - ir)) {
+        ie = 0;
+        if (++ic == chunks) {
+          ic = 0;
+          ir += kRound;
+        }
+      }
+    };
+    if (tid == 0)
+      for (int s = 0; s < kStages; ++s) issue();
+    if (!rows_done) write_rows<FMT>(p, rows, n.x, theta);
+    rows_done = true;
+    for (int r0 = 0; r0 < listed; r0 += kRound, ++round) {
+      const int ne = min(kRound, listed - r0);
+      uint64_t acc[kRound];
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x)
+      for (int e = 0; e < kRound; ++e) acc[e] = 0;
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int j0 = kCl * tp * ch + tp * rank;
+        if (chunks > 1 || round == 0) {
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-          const int j = j0 + kAppWarps * x;
-          a[x][g] = b[x][g] = make_uint4(0, 0, 0, 0);
-          if (g < ng && j < p.k_taps && q0[g] + j >= 0) {
-            const uint16_t* src = state_row(p, k[g], q0[g] + j, lane);
-            a[x][g] = first_piece(src);
-            b[x][g] = second_piece(src);
+          for (int x = 0; x < kTaps; ++x)
+            w[x] = x < tp && j0 + x < p.k_taps
+                       ? __ldg(reinterpret_cast<const unsigned long long*>(p.w + size_t(j0 + x) * kD + 64 * warp) + lane) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < kRound; ++e) {
+          if (e >= ne) break;
+          const int q = ctl.toks[r0 + e].pos + 1 + p.lookahead - p.window - p.k_taps + j0;
+          const int lo = min(max(0, -q), tp), hi = max(lo, min(tp, p.k_taps - j0));
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(stages + (got % kStages) * kStageBytes) + 32 * warp + lane;
+          if (wait_rows(&ctl, got % kStages, (got / kStages) & 1)) {
+#pragma unroll
+            for (int x = 0; x < kTaps; ++x)
+              if (x >= lo && x < hi) add2(acc[e], w[x], src[x * (kD / 2)]);
           }
-        }
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const int j = min(j0 + kAppWarps * x, p.k_taps - 1);  // (past the last tap: zero rows)
-        const ulonglong2* wr = reinterpret_cast<const ulonglong2*>(p.w + size_t(j) * kD + 8 * lane);
-        const ulonglong2 w0 = __ldg(wr), w1 = __ldg(wr + 1), w2 = __ldg(wr + 64), w3 = __ldg(wr + 65);
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-          add8(acc[g], w0, w1, a[x][g]);
-          add8(acc[g] + 4, w2, w3, b[x][g]);
+          ++got;
+          app_sync();
+          if (tid == 0) issue();
         }
       }
+      if (round && !(again && r0 == 0)) cluster_wait_acquire_div();  // (the last round's sums are read)
+#pragma unroll
+      for (int e = 0; e < kRound; ++e)
+        if (e < ne) st_dsmem_u64(dsmem_addr(part + rank * kD + 64 * warp + 2 * lane, e), acc[e]);
+      cluster_arrive_release_div();
+      cluster_wait_acquire_div();
+      cluster_arrive_release_div();
     }
-    if (r0) __syncthreads();  // the previous group's sums are read
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      if (g >= ng) break;
-      float4* dst = reinterpret_cast<float4*>(red + (size_t(warp) * kGroup + g) * kD) + lane;
-#pragma unroll
-      for (int q = 0; q < kPer / 4; ++q) {  // (conflict-free: quarter q of every lane side by side)
-        const float2 lo = pair_value(acc[g][2 * q]), hi = pair_value(acc[g][2 * q + 1]);
-        dst[32 * q] = make_float4(lo.x, lo.y, hi.x, hi.y);
-      }
-    }
-    __syncthreads();
-    if (warp < ng) {
-      float x[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) x[e] = 0.f;
-#pragma unroll 1
-      for (int ww = 0; ww < kAppWarps; ++ww) {
-        const float4* src = reinterpret_cast<const float4*>(red + (size_t(ww) * kGroup + warp) * kD) + lane;
-#pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) {
-          const float4 v = src[32 * q];
-          x[4 * q] += v.x; x[4 * q + 1] += v.y; x[4 * q + 2] += v.z; x[4 * q + 3] += v.w;
-        }
-      }
-      const Tok t = token(ents[r0 + warp]);
-      rotate_row(x, p, theta, t.pos + 1 + p.lookahead - p.window - p.stride, lane);
-      store_row<FMT>(x, lane, t.slot, p.comp_codes, p.comp_scales);
-    }
+  }
+  if (!rows_done) write_rows<FMT>(p, rows, n.x, theta);
+  pdl_trigger();  // (not earlier: the next kernel's waiting blocks would keep the clusters from starting together)
+  if (total) cluster_wait_acquire_div();  // (no CTA leaves while another may still read its list or write its sums)
+  if (tid == 0 && ctl.dead) {
+    set_status(p.status, DSV4KV_DEV_TIMEOUT);
+    uint64_t t0, t;  // copies that were in flight when the wait gave up have landed long before this
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+    do asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    while (t - t0 < 1000000ull);
   }
 }
 
@@ -623,8 +750,8 @@ __global__ void __launch_bounds__(kAppThreads) append_rows_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y, r = blockIdx.x * kAppWarps + warp, R = p.window + p.k_taps;
   const double theta = p.rope.theta_pi[lane];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (after the wait, for the same reason: 43 against 60 us a call of c128a prompts, back to back)
   const int c0 = p.cu[b], c1 = p.cu[b + 1];
   if (c0 < 0 || c1 > p.tokens || c1 - c0 > p.max_new || r >= min(c1 - c0, R)) return;  // (flagged by the entries' pass)
   const int i = c1 - 1 - r;
@@ -645,27 +772,58 @@ __global__ void __launch_bounds__(kAppThreads) append_rows_kernel(const __grid_c
   }
 }
 
-template <int FMT, bool kLong>
-cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+// Clusters of append_long_kernel that the current device holds at once.
+template <int FMT>
+int clusters_at_once() {
+  static std::atomic<int> cache[64];  // per device; 0 = not queried yet
+  std::atomic<int>& slot = cache[current_device()];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * sm_count() / kCl * kCl));
+    cfg.blockDim = dim3(kLongThreads);
+    cfg.dynamicSmemBytes = kLongSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCl;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, append_long_kernel<FMT>, &cfg) != cudaSuccess || n < 1) n = sm_count() / kCl;
+    cudaGetLastError();  // (a refused query only means a guess)
+    slot.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int FMT>
+cudaError_t launch_append(AppendParams p, cudaStream_t stream) {
+  const bool is_long = p.k_taps > kLongTaps;
   static std::atomic<uint64_t> ready{0};
-  const size_t most = kLong ? kAppWarps * kGroup * kD * sizeof(float) : kLongTaps * kD * sizeof(float);
   if (!done_on_device(ready)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(append_paged_kernel<FMT, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+    cudaError_t e = cudaFuncSetAttribute(append_paged_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(kLongTaps * kD * sizeof(float)));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(append_long_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kLongSmem));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(append_rows_kernel<FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     mark_done_on_device(ready);
   }
-  const dim3 grid(unsigned((p.tokens + p.per - 1) / p.per));
-  const size_t smem = kLong ? most : size_t(p.k_taps) * kD * sizeof(float);
-  return launch_pdl(append_paged_kernel<FMT, kLong>, grid, dim3(kAppThreads), smem, stream, p);
-}
-template <int FMT>
-cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   if (!(p.parts & kPartEntries)) {
     const dim3 grid(unsigned((std::min(p.window + p.k_taps, p.max_new) + kAppWarps - 1) / kAppWarps), unsigned(p.batch));
     return launch_pdl(append_rows_kernel<FMT>, grid, dim3(kAppThreads), 0, stream, p);
   }
-  return p.k_taps > kLongTaps ? launch_append<FMT, true>(p, stream) : launch_append<FMT, false>(p, stream);
+  // Few tokens: spread over the SMs; many: runs of up to 128 tokens (short entries, 4 CTAs an SM), or as many as the
+  // clusters that run at once share (long ones).
+  const int64_t ctas = is_long ? kCl * clusters_at_once<FMT>() : 4 * sm_count();
+  p.per = int(std::max<int64_t>(1, std::min<int64_t>((p.tokens + ctas - 1) / ctas, is_long ? kMaxTokens : 128)));
+  const int grid = int((int64_t(p.tokens) + p.per - 1) / p.per);
+  if (is_long)
+    return launch_pdl_cluster(append_long_kernel<FMT>, dim3(unsigned((grid + kCl - 1) / kCl * kCl)), dim3(kLongThreads),
+                              kLongSmem, kCl, stream, p);
+  return launch_pdl(append_paged_kernel<FMT>, dim3(unsigned(grid)), dim3(kAppThreads), size_t(p.k_taps) * kD * sizeof(float),
+                    stream, p);
 }
 
 }  // namespace
@@ -736,10 +894,6 @@ dsv4kv_status append_paged_launch(const void* s_new, const float* w, int batch, 
   p.comp_rows = comp.rows;
   p.status = static_cast<uint32_t*>(ws);
   rope_table_fill(&p.rope, rope_dim, rope_base);
-  // Few tokens: spread over the SMs; many: runs of up to 128 tokens (short entries), or long enough for two long
-  // entries (128 tokens apart in c128a) that share their weight reads.
-  const int64_t ctas = 4 * sm_count();
-  p.per = int(std::max<int64_t>(1, std::min<int64_t>((int64_t(tokens) + ctas - 1) / ctas, k_taps > kLongTaps ? kMaxTokens : 128)));
   const bool two = max_new > int64_t(lookahead) + 1;
   for (int pass = 0; pass < (two ? 2 : 1); ++pass) {
     p.parts = !two ? kPartEntries | kPartWindow | kPartRing : pass == 0 ? kPartEntries : kPartWindow | kPartRing;

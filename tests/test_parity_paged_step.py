@@ -384,3 +384,37 @@ def test_the_largest_batch():
     assert torch.equal(ring[seq, pos % (W + 8)], x)
     at = win.table[seq, (pos % W) // page].long() * page + pos % W % page
     assert torch.equal(win.codes[at], x)
+
+
+@pytest.mark.parametrize("fmt", [K.BF16, K.FP8_E4M3_ROW])
+@pytest.mark.parametrize("stride,taps,window,lookahead", [(100, 300, 128, 16), (7, 129, 20, 20), (16, 97, 0, 0)])
+def test_append_of_more_taps_than_are_summed_at_a_time(fmt, stride, taps, window, lookahead):
+    a = Appender(190 + taps, 3, fmt, stride, taps, window, lookahead, 1500)
+    for counts in ([700, 1, 40], [1, 0, 3], [2, 2, 1], [300, 500, 80], [1, 1, 1], [0, 90, 333]):
+        a.step(counts)
+    a.check()
+
+
+def test_append_of_many_long_entries():
+    """Every token emits an entry of 40 taps, which all weigh nothing but the 14th."""
+    n, taps = 9000, 40
+    rng = np.random.default_rng(3)
+    table = torch.from_numpy(rng.permutation(2 * 141).reshape(2, 141).astype(np.int32)).cuda()
+    comp = K.PagedCache(0, torch.zeros(2 * 141 * 64, 512, dtype=torch.bfloat16, device="cuda"), table, 64)
+    w = torch.zeros(taps, 512, device="cuda")
+    w[13] = 1.0
+    ring = torch.zeros(2, taps, 512, dtype=torch.bfloat16, device="cuda")
+    ws = K.new_workspace(K.paged_step_workspace_bytes(2))
+    x = torch.from_numpy(rng.normal(size=(2, n, 512)).astype(np.float32)).to(torch.bfloat16).cuda()
+    old = 0
+    for new in (n - 1000, n):           # (the second call reads the first one's ring)
+        m = K.slot_map(dev([old] * 2, torch.int64), dev([new] * 2, torch.int64), comp, None, 2 * (new - old), n, window=0,
+                       stride=1, lookahead=0, ws=ws)
+        K.append_paged(x[:, old:new].reshape(-1, 512).contiguous(), w, m, ring, None, comp, stride=1, window=0,
+                       lookahead=0, rope_dim=0, ws=ws)
+        old = new
+    assert K.workspace_status(ws) == 0
+    e = torch.arange(n, device="cuda")
+    for b in range(2):
+        got = comp.codes[table[b][e // 64].long() * 64 + e % 64]
+        assert not got[:26].any() and torch.equal(got[26:], x[b, :n - 26])
