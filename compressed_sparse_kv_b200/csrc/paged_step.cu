@@ -18,18 +18,34 @@
 // thread finds the sequence of its first token by binary search and walks on;
 // 4 tokens a thread, 16-byte stores.
 //
-// append_paged_kernel.  A CTA of 8 warps takes `per` consecutive tokens.  It
-// lists the tokens whose row stays in a ring and those that emit an entry; a
-// warp copies / rotates one row (16 channels a lane); entries of up to 32
-// taps are one warp's work, longer ones (c128a) are summed by all 8 warps,
-// tap j by warp j % 8, four entries at a time so that a weight row (2 KB) is
-// read once for four state rows, the warps' sums added in warp order.  The
-// work is bound by the state rows' HBM reads for whole prompts and by
-// latency for a decode step.  Entries read rows of the raw ring that tokens of the
+// (48 prompts of up to 65,536 tokens, about 1.7 M in all: tables and map 21 us for 35 MB, bound by the map's divisions; a decode step of
+// 32 sequences: 8.0 us, two launches' latency.)
+//
+// append_paged_kernel (entries of up to 32 taps).  A CTA of 8 warps takes `per`
+// consecutive tokens.  It lists the tokens whose row stays in a ring and those
+// that emit an entry; a warp copies / rotates one row or sums one entry
+// (16 channels a lane, the weights in shared memory, packed fp32 multiply-adds).
+// Whole prompts are bound by instructions and the rows' HBM reads: 75,000
+// tokens of c4a, 96 MB, in 31 us (3.1 TB/s, its second launch included); a step
+// of 32 sequences x 8 tokens, 5.3 us, is latency.  Taps loaded one address at
+// a time and scalar multiply-adds: 38 us; 3 CTAs an SM at 80 registers: 42.
+//
+// append_long_kernel (more taps, c128a).  Every state row is read once but the
+// weights, 2 KB a tap, would be read again for each entry; so a cluster of 8 CTAs
+// shares the entries of its tokens, CTA r keeping the weights of taps
+// [16 r, 16 r + 16) in registers (two channels a thread).  An entry's 16 rows are
+// one bulk copy (four entries in flight), the CTAs' sums of 8 entries are
+// exchanged through distributed shared memory, and a ninth warp of each CTA
+// adds up and stores one of them while the others go on.  110,000 tokens of
+// c128a, 124 MB, take 43 us (2.9 TB/s; one CTA an entry with its weights from L2:
+// 51), a step of 61 sequences 8.6 us (12.0).
+//
+// Entries read rows of the raw ring that tokens of the
 // same call replace when a sequence has more than lookahead + 1 new ones
 // (entry taps reach back to p + 1 + lookahead - (window + k_taps), the row
 // replaced by token p' is p' - (window + k_taps)); the ring
-// (and the window, whose rows are the last ones too) is then written by a second launch, one warp a row.
+// (and the window, whose rows are the last ones too) is then written by a
+// second launch, append_rows_kernel, one warp a row (5 us of the prompts' times).
 #include <cmath>
 #include <cstdint>
 

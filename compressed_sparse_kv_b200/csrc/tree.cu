@@ -23,17 +23,26 @@
 // load waited for the value product, and 64-column products ran at half rate.
 //   * S = Q . R^T: M = 128 queries, N = 128 rows, 32 K-steps; two buffers, so the
 //     next tile's scores are formed while this one's softmax runs;
-//   * 16 softmax warps a CTA, one query and 16 rows a thread (TMEM lanes 0-63: the
+//   * 8 softmax warps a CTA, one query and 32 rows a thread (TMEM lanes 0-63: the
 //     queries against rows 0-63, lanes 64-127: against rows 64-127): the weights
 //     2^(x - m) against a running maximum m that is raised only when some score
-//     passes it by 2^8 (one vote a tile), rounded to 16 bits; their sum is kept
-//     per thread and added up once per group;
+//     passes it by 2^8 (one vote a tile), rounded to 16 bits, the products'
+//     operand type (half a step of a weight, far below the rows' own rounding);
+//     their sum, in fp32, is kept per thread and added up once per group;
 //   * O += P . R: M = 128, N = 256, 8 K-steps, twice.
 // Keys and values have their own barriers: a key buffer is refilled as soon as its
 // scores are formed, a value buffer when its product is done.  Rows come by TMA
 // (whole tiles of bf16 rows; both CTAs' copies complete on the first CTA's
 // barrier) or through loader warps: 16-byte cp.async, or dequantisation to f16 as
 // in the decode kernel.
+//
+// What bounds it: a buffer's round (product done, copy issued, rows here, product
+// issued), since keys and values have one buffer each in two halves.  Measured
+// per tile of 128 rows and pair of CTAs: 2.2 us for whole bf16 tiles (256 x 64
+// query rows x 8,320 rows x 4 sequences: 216 us, 856 TFLOP/s; the products alone
+// would take 1.0 us), 3.2 us for selected bf16 rows, 4.2 us for fp8 rows.
+// 18 us of latency for one short sequence: 4 us until the schedule and the tree
+// are known, two tiles of 4 us each (not overlapped), 3 us to finish.
 //
 // Work split.  When the groups fill the pairs evenly a pair takes whole groups
 // (c, c + P, ...); otherwise the tiles of all groups are laid end to end and cut
@@ -78,8 +87,7 @@ constexpr uint32_t kColS = 256;  // S: 2 buffers of 64 columns
 constexpr float kRaise = 8.0f;   // log2 units a score may pass the running maximum by
 constexpr float kNoMax = -3.4028235e38f;  // a maximum that nothing has reached yet (finite: x - m of a hidden row is -inf)
 // Tiles that cut groups may cost (partial sums, a second part per pair, the merge) before whole groups take longer.
-// Whole groups of 10 tiles against runs of 7: 43 against 53 us; 12 against 7: 80 against 60; 10 against 6 (fp8): 89
-// against 71; 18 against 11 (fp8): 99 against 78.
+// Whole groups of 10 tiles against runs of 7: 37 against 48 us; 12 against 8 (selected, fp8): 77 against 62 us.
 constexpr int kSplitCost = 3;
 // Row scales below this are taken as it: the weight of a stored row carries its scale and the denominator divides it
 // out again, which needs a normal reciprocal.  Such a row's values are below 2^-91.
@@ -93,7 +101,8 @@ constexpr int kChans = 128;  // output channels per softmax thread
 
 // Warps: 0 schedule and queries, 1 products, 2-5 keys, 6-9 values, then 8 for the softmax and epilogue.  (16 softmax
 // warps leave 72 registers a thread: 241 against 223 us for long dense contexts in bf16, and quantised rows want the
-// registers for 8 loads of 16 bytes in flight; 2 value warps: 56 against 53 us for selected rows.)
+// registers for 8 loads of 16 bytes in flight; 2 value warps: 56 against 53 us for selected rows; two batches of 4 loads
+// instead of one of 8: 67 against 62 us for selected fp8 rows.)
 template <int FMT>
 struct Cfg {
   static constexpr bool kQuant = FMT != DSV4KV_BF16;
