@@ -1242,22 +1242,25 @@ __global__ void __launch_bounds__(256) tree_combine(const __grid_constant__ Para
   const int j = (blockIdx.x & 15) * 8 + warp;
   pdl_trigger();
   pdl_wait();
+  // (most groups are cut once: the next run's record is read along with the first one's)
+  const bool any = c + 1 < P;
   const Rec own = p.rec[2 * c + 1];
+  Rec r = p.rec[any ? 2 * c + 2 : 2 * c];
+  const float4 ml0 = p.ml[size_t(2 * c + 1) * kGroup + j], ml1 = p.ml[size_t(any ? 2 * c + 2 : 2 * c) * kGroup + j];
   if (!own.valid) return;
-  const float4 ml0 = p.ml[size_t(2 * c + 1) * kGroup + j];
   const int pos = __float_as_int(ml0.z), row = __float_as_int(ml0.w);
   if (row < 0) return;
   // the runs behind it: first slots of the next pairs, until one ends the group
   float M = ml0.x;
   int last = c;
   for (int end = own.t1; end < own.tiles && last + 1 < P; ++last) {
-    const Rec r = p.rec[2 * (last + 1)];
+    if (last > c) r = p.rec[2 * (last + 1)];
     if (!r.valid || r.b != own.b || r.g != own.g) {  // (a run that timed out)
       if (lane == 0) set_status(p.status, DSV4KV_DEV_INCONSISTENT);
       return;
     }
     end = r.t1;
-    M = fmaxf(M, p.ml[size_t(2 * (last + 1)) * kGroup + j].x);
+    M = fmaxf(M, last > c ? p.ml[size_t(2 * (last + 1)) * kGroup + j].x : ml1.x);
   }
   float L = 0.f;
   float4 o[4];
@@ -1265,7 +1268,7 @@ __global__ void __launch_bounds__(256) tree_combine(const __grid_constant__ Para
   for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int x = c; x <= last; ++x) {
     const size_t slot = x == c ? 2 * c + 1 : 2 * x;
-    const float4 ml = p.ml[slot * kGroup + j];
+    const float4 ml = x == c ? ml0 : x == c + 1 ? ml1 : p.ml[slot * kGroup + j];
     if (ml.y == 0.f) continue;  // it saw no row (its O may be unwritten)
     const float w = exp2_approx(ml.x - M);
     L = fmaf(w, ml.y, L);
