@@ -18,8 +18,8 @@
 // thread finds the sequence of its first token by binary search and walks on;
 // 4 tokens a thread, 16-byte stores.
 //
-// (48 prompts of up to 65,536 tokens, about 1.7 M in all: tables and map 21 us for 35 MB, bound by the map's divisions; a decode step of
-// 32 sequences: 8.0 us, two launches' latency.)
+// (48 prompts of up to 65,536 tokens, about 1.7 M in all: tables and map 19.5 us for 35 MB, bound by start-up and searches; a decode step of
+// 32 sequences: 7.2 us, two launches' latency.  Plain integer divisions: 21.3 and 8.0.)
 //
 // append_paged_kernel (entries of up to 32 taps).  A CTA of 8 warps takes `per`
 // consecutive tokens.  It lists the tokens whose row stays in a ring and those
@@ -184,6 +184,15 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TablePar
   }
 }
 
+// Quotients by a divisor of the whole call: floor(n / d) is the high word of n * (floor((2^64 - 1) / d) + 1) for all 32-bit
+// n and d > 1 (Lemire, Kaser and Kurz, "Faster remainder by direct computation", 2019).
+struct Div {
+  uint64_t m;
+  int d;
+  explicit Div(int by) : m(by > 1 ? ~uint64_t(0) / uint64_t(by) + 1 : 0), d(by) {}
+  __device__ __forceinline__ int quot(int n) const { return d == 1 ? n : int(__umul64hi(m, uint64_t(uint32_t(n)))); }
+};
+
 struct SlotParams {
   const int64_t *t_old, *t_new;
   int batch;
@@ -195,10 +204,11 @@ struct SlotParams {
   int64_t* pos;
   int32_t *win_slot, *comp_slot;
   uint32_t* status;
+  Div by_window, by_stride, by_comp, by_win;  // window (1 without one), stride, rows a page
 };
 
-__device__ __forceinline__ int32_t slot_of(const PageDesc& d, int b, int row, uint32_t* status) {
-  const int page = row / d.page_rows;
+__device__ __forceinline__ int32_t slot_of(const PageDesc& d, const Div& by, int b, int row, uint32_t* status) {
+  const int page = by.quot(row);
   const int32_t pg = __ldg(d.table + size_t(b) * d.table_stride + page);
   if (pg < 0 || pg >= d.pool_pages) {
     set_status(status, DSV4KV_DEV_BAD_PAGE);
@@ -254,9 +264,12 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const SlotParams
       const int pp = o + (i - pre[b]);
       sq[e] = b;
       ps[e] = pp;
-      if (p.win.table && pp >= n - p.window) ws[e] = slot_of(p.win, b, pp % p.window, p.status);
+      if (p.win.table && pp >= n - p.window) ws[e] = slot_of(p.win, p.by_win, b, pp - p.by_window.quot(pp) * p.window, p.status);
       const int r = pp + 1 + p.lookahead - p.window;  // the entry ends when it is a multiple of the stride
-      if (p.comp.table && r > 0 && r % p.stride == 0) cs[e] = slot_of(p.comp, b, r / p.stride - 1, p.status);
+      if (p.comp.table && r > 0) {
+        const int n_e = p.by_stride.quot(r);
+        if (n_e * p.stride == r) cs[e] = slot_of(p.comp, p.by_comp, b, n_e - 1, p.status);
+      }
     }
     if (i0 + kSlotPer <= p.capacity) {
       *reinterpret_cast<int4*>(p.seq + i0) = make_int4(sq[0], sq[1], sq[2], sq[3]);
@@ -868,7 +881,8 @@ dsv4kv_status slot_map_launch(const int64_t* t_old, const int64_t* t_new, int ba
                               int32_t* cu, int32_t* seq, int64_t* pos, int32_t* win_slot, int32_t* comp_slot, void* ws,
                               cudaStream_t stream) {
   const SlotParams p{t_old, t_new, batch, t_max, window, stride, lookahead, comp, win, capacity, cu, seq, pos,
-                     win_slot, comp_slot, static_cast<uint32_t*>(ws)};
+                     win_slot, comp_slot, static_cast<uint32_t*>(ws), Div(std::max(window, 1)), Div(stride),
+                     Div(comp.page_rows), Div(win.page_rows)};
   const int per = kSlotThreads * kSlotPer;
   const int grid = int(std::max<int64_t>(1, std::min<int64_t>(4 * sm_count(), (int64_t(capacity) + per - 1) / per)));
   const size_t smem = size_t(3 * batch + 1) * sizeof(int32_t);
