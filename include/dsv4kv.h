@@ -524,6 +524,7 @@ dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t bat
  * nodes * heads < 2^31; a pool of no pages only where no sequence up to t_max
  * can have a row of it; 1 <= batch <= 1024; the three caches of one format;
  * 1 <= k <= 2048 with idx; stride >= 1; 0 <= window <= 65536; t_max < 2^30.
+ * The 128-row tiles of all groups of 128 query rows (idx: of all nodes), at t_max, number fewer than 2^31 - 4096.
  * ------------------------------------------------------------------------ */
 /* (k = 0: the dense form, idx NULL) */
 size_t dsv4kv_tree_decode_paged_workspace_bytes(int32_t batch, int32_t heads, int32_t dim, int32_t max_nodes,

@@ -418,3 +418,50 @@ def test_append_of_many_long_entries():
     for b in range(2):
         got = comp.codes[table[b][e // 64].long() * 64 + e % 64]
         assert not got[:26].any() and torch.equal(got[26:], x[b, :n - 26])
+
+
+@pytest.mark.parametrize("stride,taps", [(4, 8), (128, 128)])
+def test_append_replayed_and_on_two_streams(stride, taps):
+    """A captured append replayed on new states, and two appends at once on streams and workspaces of their own."""
+    W, t, page = 128, [900, 31, 400], 64
+    rng = np.random.default_rng(12)
+    rows = [S.cache_rows(x, W, stride, 0) for x in t]
+    width = max(1, *(-(-r // page) for r in rows))
+    table = dev(rng.permutation(3 * width).reshape(3, width).tolist())
+    wtable = dev(rng.permutation(6).reshape(3, 2).tolist())
+    w = torch.softmax(torch.from_numpy(rng.normal(size=(taps, 512)).astype(np.float32)).cuda(), 0)
+    new = lambda: (K.PagedCache(0, torch.zeros(3 * width * page, 512, dtype=torch.bfloat16, device="cuda"), table, page),  # noqa: E731
+                   K.PagedCache(0, torch.zeros(6 * page, 512, dtype=torch.bfloat16, device="cuda"), wtable, page),
+                   torch.zeros(3, W + taps, 512, dtype=torch.bfloat16, device="cuda"), K.new_workspace(16))
+    first, _, _, ws0 = new()
+    m = K.slot_map(dev([0, 0, 0], torch.int64), dev(t, torch.int64), first, new()[1], sum(t), max(t), window=W,
+                   stride=stride, lookahead=0, ws=ws0)
+    x = [torch.from_numpy(rng.normal(size=(sum(t), 512)).astype(np.float32)).to(torch.bfloat16).cuda() for _ in range(2)]
+
+    def run(states, c, stream=None):
+        K.append_paged(states, w, m, c[2], c[1], c[0], stride=stride, window=W, lookahead=0, ws=c[3], stream=stream)
+
+    want = [new() for _ in x]
+    for s, c in zip(x, want):
+        run(s, c)
+    torch.cuda.synchronize()
+
+    def same(c, d):
+        return all(torch.equal(a, b) for a, b in ((c[0].codes, d[0].codes), (c[1].codes, d[1].codes), (c[2], d[2])))
+    static, c = x[0].clone(), new()
+    run(static, c)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(static, c)
+    for s, d in zip(x[::-1] + x, want[::-1] + want):
+        static.copy_(s)
+        g.replay()
+        assert same(c, d)
+    streams, got = [torch.cuda.Stream() for _ in x], [new() for _ in x]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, c, st in zip(x, got, streams):
+            run(s, c, stream=st)
+    torch.cuda.synchronize()
+    assert all(same(c, d) and K.workspace_status(c[3]) == 0 for c, d in zip(got, want))
