@@ -870,6 +870,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tmem_wait_st();
             }
+            // The next product adds to all 128 lanes but waits for one half's weights only (p_full[h]): no warp hands
+            // over weights until all of them have rescaled their lanes.
+            tc_fence_before();
+            soft_sync();
+            tc_fence_after();
           }
         }
         uint32_t pk[kCols / 2];
