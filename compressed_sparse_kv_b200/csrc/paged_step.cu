@@ -3,14 +3,14 @@
 // paragraph: blocks of a shared pool; "compressor-state blocks").
 //
 // block_table_kernel.  With pages(t) = ceil(rows(t) / page_rows), sequence b
-// gives back G_b = max(0, pages(t_old) - pages(t_new)) pages or takes
-// A_b = max(0, pages(t_new) - pages(t_old)).  Given-back pages are pushed on the
-// free stack in (b, entry) order, then A = sum A_b are popped in (b, entry)
-// order: taken page a is element count + G - 1 - a of the grown stack.  An
-// element past the old count is read where it comes from, in a shrinking
-// sequence's table row, so pushes and pops need no order between them and
-// one launch does both: every CTA forms the two prefix sums over the batch
-// (one pass of warp scans in shared memory) and takes a share of the pages.
+// gives back entries [pages(t_new), pages(t_old)) of its table row or takes
+// A_b = max(0, pages(t_new) - pages(t_old)) pages.  The G pages among the entries
+// given back are pushed on the free stack in (b, entry) order, then A = sum A_b are
+// popped in (b, entry) order: taken page a is element count + G - 1 - a of the
+// grown stack.  An element past the old count is read where it comes from, in a
+// shrinking sequence's table row, so pushes and pops need no order between them
+// and one launch does both: every CTA forms the prefix sums over the batch
+// (passes of warp scans in shared memory) and takes a share of the pages.
 // The count is read by every CTA and written by the last one to finish, so
 // that it may be updated in place.
 //
@@ -121,7 +121,8 @@ __device__ __forceinline__ int pages_of(const TableParams& p, int64_t t) {
 
 __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableParams p) {
   extern __shared__ int32_t sm[];
-  int32_t *back = sm, *take = sm + p.batch + 1;  // prefix sums of the pages given back / taken
+  int32_t *back = sm, *take = back + p.batch + 1;          // prefix sums of the entries given back / taken
+  int32_t *first = take + p.batch + 1, *good = first + p.batch + 1;  // a sequence's first such entry; see below
   pdl_trigger();
   pdl_wait();
   int64_t count = *p.free_count;
@@ -134,6 +135,8 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TablePar
       [&](int b) -> uint64_t {
         const int o = pages_of(p, clamp_len(p.t_old[b], p.t_max, p.status));
         const int n = pages_of(p, clamp_len(p.t_new[b], p.t_max, p.status));
+        first[b] = min(o, n);
+        good[b] = 0;
         return o > n ? uint64_t(o - n) : uint64_t(n - o) << 32;
       },
       [&](int b, uint64_t v) {
@@ -141,36 +144,72 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TablePar
         take[b] = int32_t(v >> 32);
       });
   const int G = int(sums & 0xffffffffu), A = int(sums >> 32);
+  if (threadIdx.x == 0) back[p.batch] = G;
   __syncthreads();
-  const int step = gridDim.x * kTabThreads, first = blockIdx.x * kTabThreads + int(threadIdx.x);
-  // the table entry that given-back page r comes from
-  auto given = [&](int r) -> int32_t {
+  auto entry = [&](int b, int j) { return p.table[size_t(b) * p.table_stride + first[b] + j]; };
+  auto is_page = [&](int32_t pg) { return pg >= 0 && pg < p.pool_pages; };
+  // Entries that hold no page (-1: the stack had none left when they were taken) are not given back.  Every CTA looks at
+  // all of them; where there are any, good[] becomes the prefix sums of the pages and the ranks below are counted out.
+  bool any = false;
+  for (int r = threadIdx.x; r < G; r += kTabThreads) {
     const int b = find_seq(back, p.batch, r);
-    const int n = pages_of(p, clamp_len(p.t_new[b], p.t_max, nullptr));
-    return p.table[size_t(b) * p.table_stride + n + (r - back[b])];
+    if (!is_page(entry(b, r - back[b]))) {
+      atomicAdd(&good[b], 1);
+      any = true;
+    }
+  }
+  any = __syncthreads_or(any);
+  int pages = G;
+  if (any) {
+    pages = int(block_prefix<kTabThreads>(
+        p.batch, [&](int b) -> uint64_t { return uint64_t(back[b + 1] - back[b] - good[b]); },
+        [&](int b, uint64_t v) { good[b] = int32_t(v); }));
+    if (threadIdx.x == 0) good[p.batch] = pages;
+    __syncthreads();
+  }
+  auto whole = [&](int b) { return good[b + 1] - good[b] == back[b + 1] - back[b]; };  // (where any)
+  const int step = gridDim.x * kTabThreads, begin = blockIdx.x * kTabThreads + int(threadIdx.x);
+  // page number r of those given back
+  auto given = [&](int r) -> int32_t {
+    const int b = find_seq(any ? good : back, p.batch, r);
+    int j = r - (any ? good[b] : back[b]);
+    if (any && !whole(b)) {
+      int k = j;
+      for (j = 0; !is_page(entry(b, j)) || k-- > 0;) ++j;  // (ends: the sequence gives back more than k pages)
+    }
+    return entry(b, j);
   };
-  for (int r = first; r < G; r += step) {
-    const int32_t pg = given(r);
-    if (pg < 0 || pg >= p.pool_pages) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+  for (int x = begin; x < G; x += step) {
+    const int b = find_seq(back, p.batch, x), j = x - back[b];
+    const int32_t pg = entry(b, j);
+    if (!is_page(pg)) {
+      if (pg != -1) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+      continue;
+    }
+    int r = x;
+    if (any) {
+      r = good[b] + j;
+      if (!whole(b))
+        for (int i = 0; i < j; ++i) r -= !is_page(entry(b, i));
+    }
     if (count + r < p.free_cap) p.free_pages[count + r] = pg;
     else set_status(p.status, DSV4KV_DEV_NO_PAGES);
   }
-  const int64_t top = min(count + G, p.free_cap);  // the grown stack
-  for (int a = first; a < A; a += step) {
+  const int64_t top = min(count + pages, p.free_cap);  // the grown stack
+  for (int a = begin; a < A; a += step) {
     const int b = find_seq(take, p.batch, a);
-    const int o = pages_of(p, clamp_len(p.t_old[b], p.t_max, nullptr));
     const int64_t at = top - 1 - a;
     int32_t pg = -1;
     if (at < 0) {
       set_status(p.status, DSV4KV_DEV_NO_PAGES);
     } else {
       pg = at >= count ? given(int(at - count)) : p.free_pages[at];
-      if (pg < 0 || pg >= p.pool_pages) {
+      if (!is_page(pg)) {
         set_status(p.status, DSV4KV_DEV_BAD_PAGE);
         pg = -1;
       }
     }
-    p.table[size_t(b) * p.table_stride + o + (a - take[b])] = pg;
+    p.table[size_t(b) * p.table_stride + first[b] + (a - take[b])] = pg;
   }
   // the last CTA to get here (every CTA has read the count) writes it
   __syncthreads();
@@ -872,7 +911,12 @@ dsv4kv_status block_table_update_launch(const int64_t* t_old, const int64_t* t_n
   // a decode step changes at most a page or so per sequence; prompts bring up to table_stride of them
   const int64_t most = int64_t(batch) * table_stride;
   const int grid = int(std::max<int64_t>(1, std::min<int64_t>(64, most / (2 * kTabThreads))));
-  launch_pdl(block_table_kernel, dim3(grid), dim3(kTabThreads), size_t(2 * (batch + 1)) * sizeof(int32_t), stream, p);
+  const size_t smem = size_t(4 * (batch + 1)) * sizeof(int32_t);
+  if (smem > 48 * 1024 - 256) {  // (more than 3054 sequences)
+    const cudaError_t e = cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return set_error(DSV4KV_ERR_CUDA, "block_table_kernel: %s", cudaGetErrorString(e));
+  }
+  launch_pdl(block_table_kernel, dim3(grid), dim3(kTabThreads), smem, stream, p);
   return check_launch("block_table_kernel");
 }
 

@@ -391,14 +391,17 @@ dsv4kv_status dsv4kv_dense_decode_paged(const void* q, const dsv4kv_paged_cache*
  * int32 [free_cap]) is a stack of *free_count free page numbers.
  *   1. Sequences that shrink give back table[b][pages(t_new) .. pages(t_old)):
  *      pushed in ascending (b, entry) order.  Their table entries keep the
- *      old numbers (nothing reads past a sequence's rows).
+ *      old numbers (nothing reads past a sequence's rows).  An entry that
+ *      holds no page of the pool is not pushed: -1 (the stack had run out when
+ *      it was taken) silently, any other with DSV4KV_DEV_BAD_PAGE.
  *   2. Sequences that grow fill table[b][pages(t_old) .. pages(t_new)) in
  *      ascending (b, entry) order, each entry popped from the end of the stack.
  * *free_count_out is the count after both.  It may be free_count itself (a
  * captured step that is replayed); with another word the call can be repeated
  * on the same inputs with the same result.  A stack that runs out gives
  * entries of -1 and one that would exceed free_cap drops pages, both with
- * DSV4KV_DEV_NO_PAGES; a page number outside [0, pool_pages) sets
+ * DSV4KV_DEV_NO_PAGES; an entry of -1 stays until its sequence gives it back.
+ * A page number on the stack outside [0, pool_pages) sets
  * DSV4KV_DEV_BAD_PAGE and is never handed out (the entry becomes -1); a
  * length outside [0, t_max] or a count outside [0, free_cap] is clamped and
  * sets DSV4KV_DEV_BAD_LENGTH.

@@ -8,7 +8,7 @@ Test infrastructure: only the tests use this module.
 Readings adopted (the pages give none of these):
 * pages are taken from and given back to a stack of free page numbers, one
   sequence after the other; everything given back is pushed before anything
-  is taken;
+  is taken; an entry that got no page (-1) gives none back;
 * a drafted node at position p attends as the token at p would with its
   ancestors appended to the caches: entries [0, N(p)), window positions
   [p - W, t), its strict ancestors;
@@ -35,7 +35,8 @@ def block_table_update(t_old, t_new, table, free, page_rows: int, window: int, s
     pages = [[-(-cache_rows(t, window, stride, lookahead) // page_rows) for t in ts] for ts in (t_old, t_new)]
     for b, (o, n) in enumerate(zip(*pages)):
         for j in range(n, o):
-            free.append(table[b][j])
+            if table[b][j] >= 0:
+                free.append(table[b][j])
     for b, (o, n) in enumerate(zip(*pages)):
         for j in range(o, n):
             table[b][j] = free.pop() if free else -1

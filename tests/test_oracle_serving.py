@@ -76,3 +76,10 @@ def test_a_node_without_rows_gives_zeros():
     q = np.ones((2, 1, 128))
     out = S.tree_decode(q, np.zeros((0, 128)), np.zeros((0, 128)), np.ones((2, 128)), [-1, 0], 0, 8, 4)
     assert np.all(out[0] == 0) and np.any(out[1] != 0)
+
+
+def test_entries_without_a_page_give_none_back():
+    t, f = S.block_table_update([0, 0], [12, 20], [[-1] * 5, [-1] * 5], [4, 9, 1, 7], 4, 0, 1)
+    assert t == [[7, 1, 9, -1, -1], [4, -1, -1, -1, -1]] and f == []
+    t, f = S.block_table_update([12, 20], [4, 0], t, f, 4, 0, 1)
+    assert f == [1, 9, 4]                                             # and 7 is still the first sequence's

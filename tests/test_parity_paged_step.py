@@ -465,3 +465,46 @@ def test_append_replayed_and_on_two_streams(stride, taps):
             run(s, c, stream=st)
     torch.cuda.synchronize()
     assert all(same(c, d) and K.workspace_status(c[3]) == 0 for c, d in zip(got, want))
+
+
+@pytest.mark.parametrize("batch,pool", [(3, 10), (40, 700), (4096, 5000)])
+def test_a_stack_that_ran_out_is_whole_again(batch, pool):
+    """More pages are asked for than there are, over several steps, some are given back in between (runs with and without
+    pages in any mixture), in the end all: the stack then holds the pool's pages, and admits again."""
+    rng = np.random.default_rng(batch)
+    page, width = 64, 24
+    table, free = [[-1] * width for _ in range(batch)], [int(x) for x in rng.permutation(pool)]
+    pages, fl = K.PageTable(dev(table), page, pool), dev(free)
+    count, ws, t = dev([pool], torch.int64), K.new_workspace(K.paged_step_workspace_bytes(batch)), [0] * batch
+
+    def step(new, flags):
+        nonlocal table, free, t
+        table, free = S.block_table_update(t, new, table, free, page, 0, 1)
+        K.block_table_update(dev(t, torch.int64), dev(new, torch.int64), pages, fl, count, page * width, window=0, stride=1,
+                             free_count_out=count, ws=ws)
+        assert count.item() == len(free) and fl[:len(free)].tolist() == free and pages.table.tolist() == table
+        assert K.workspace_status(ws) == flags
+        ws.zero_()
+        t = new
+
+    most = pool * page * 13 // (10 * batch)
+    step([min(page * width, int(x)) for x in rng.integers(most, 2 * most, batch)], K.DEV_NO_PAGES)
+    for _ in range(4):
+        ran_out = len(free)
+        new = [int(x) for x in np.where(rng.random(batch) < 0.5, rng.integers(0, page * width + 1, batch), t)]
+        asked = sum(max(0, -(-b // page) - -(-a // page)) for a, b in zip(t, new))
+        back = sum(sum(x >= 0 for x in table[i][-(-b // page):-(-a // page)]) for i, (a, b) in enumerate(zip(t, new)))
+        step(new, K.DEV_NO_PAGES if asked > ran_out + back else 0)
+    step([0] * batch, 0)
+    assert sorted(free) == list(range(pool))
+    some = [page * (pool // batch)] * batch if pool // batch <= width else [page * width] * batch
+    step(some, 0)
+    assert min(min(r[:some[0] // page]) for r in table) >= 0
+
+
+def test_entries_outside_the_pool_are_not_given_back():
+    ws, fl, count = K.new_workspace(16), dev([3, 0, 0, 0, 0, 0, 0, 0]), dev([1], torch.int64)
+    p = K.PageTable(dev([[4, 99, 6, -5, 1], [-1, 2, -1, -1, -1]]), 64, 8)
+    out = K.block_table_update(dev([320, 128], torch.int64), dev([0, 0], torch.int64), p, fl, count, 320, window=0, stride=1,
+                               ws=ws)
+    assert K.workspace_status(ws) == K.DEV_BAD_PAGE and out.item() == 5 and fl[:5].tolist() == [3, 4, 6, 1, 2]
