@@ -221,6 +221,7 @@ class SlotMap:
 # The serving-step calls run once per layer and step, so their checks are written to cost well under a microsecond each:
 # every tensor is dense, of its type, on the call's device (its index) and of its shape.
 _I32, _I64, _F32, _BF, _U8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
+_BF_WORDS = (torch.bfloat16, torch.uint16, torch.int16)      # bf16 rows may come as 16-bit words
 _PAGED = struct.Struct("@iiiiqPPP")   # dsv4kv_paged_cache
 _CACHE = struct.Struct("@iiqPP")      # dsv4kv_cache
 _TABLE = struct.Struct("@Piiq")       # dsv4kv_page_table
@@ -254,17 +255,22 @@ _SCALE_BYTES = {FP8_E4M3_ROW: 4, FP4_E2M1_G16: 32, FP8_E4M3_ROW_ROPE_BF16: 4}
 
 
 def _rows(c, rows: int, dev: int, where: str, name: str) -> tuple[int, int]:
-    """(codes, scales) of a 512-channel cache that holds at least `rows` rows, densely, on the device."""
-    t = c.codes
-    per = _ROW_BYTES.get(c.fmt, 0) if c.dim == 512 else 0      # (else: the library's own refusal)
+    """(codes, scales) of a 512-channel cache that holds at least `rows` rows, densely, of its format's types, on the
+    device."""
+    t, fmt = c.codes, c.fmt
+    per = _ROW_BYTES.get(fmt, 0) if c.dim == 512 else 0        # (else: the library's own refusal)
     if t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < rows * per:
         raise ValueError(f"{where}: {name}.codes must be contiguous, on device {dev}, and hold {rows} rows")
-    if c.fmt == BF16:
+    if t.dtype not in _BF_WORDS if fmt == BF16 else fmt in _SCALE_BYTES and t.element_size() != 1:
+        raise ValueError(f"{where}: {name}.codes must be {'bf16' if fmt == BF16 else 'bytes'}, got {t.dtype}")
+    if fmt == BF16:
         return t.data_ptr(), 0
     s = c.scales
     if s is None or s.get_device() != dev or not s.is_contiguous() or (
-            per and s.numel() * s.element_size() < rows * _SCALE_BYTES[c.fmt]):
+            per and s.numel() * s.element_size() < rows * _SCALE_BYTES[fmt]):
         raise ValueError(f"{where}: {name}.scales must be contiguous, on device {dev}, and hold {rows} rows")
+    if s.element_size() != 1 if fmt == FP4_E2M1_G16 else fmt in _SCALE_BYTES and s.dtype is not _F32:
+        raise ValueError(f"{where}: {name}.scales must be {'bytes' if fmt == FP4_E2M1_G16 else 'float32'}, got {s.dtype}")
     return t.data_ptr(), s.data_ptr()
 
 

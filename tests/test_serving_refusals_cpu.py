@@ -158,3 +158,37 @@ def test_the_binding_refuses_what_it_cannot_marshal():
         K.tree_decode_paged(q, c, c, d, cu, torch.zeros(3, dtype=torch.int64), i64, 100, 4)
     with pytest.raises(ValueError, match="q must"):
         K.tree_decode_paged(q.float(), c, c, d, cu, torch.zeros(3, dtype=torch.int32), i64, 100, 4)
+
+
+@pytest.mark.parametrize("fmt,codes,scales,text", [
+    (0, torch.float32, None, "comp.codes"), (0, torch.float16, None, "comp.codes"), (0, torch.uint8, None, "comp.codes"),
+    (1, torch.bfloat16, torch.float32, "comp.codes"), (1, torch.uint8, torch.float64, "comp.scales"),
+    (1, torch.uint8, torch.bfloat16, "comp.scales"), (1, torch.uint8, torch.int32, "comp.scales"),
+    (2, torch.int32, torch.uint8, "comp.codes"), (2, torch.uint8, torch.float32, "comp.scales"),
+    (3, torch.float16, torch.float32, "comp.codes"), (3, torch.uint8, torch.float16, "comp.scales"),
+])
+def test_the_binding_refuses_rows_of_another_type(fmt, codes, scales, text):
+    """Tensors with room for the rows, whose bytes would be taken for something else."""
+    m = K.new_slot_map(2, 8, device="cpu")
+    x, w, ring = torch.zeros(8, 512, dtype=torch.bfloat16), torch.zeros(8, 512), torch.zeros(2, 136, 512, dtype=torch.bfloat16)
+    c = K.PagedCache(fmt, torch.zeros(128, 1024, dtype=codes), torch.zeros(2, 4, dtype=torch.int32), 64,
+                     None if scales is None else torch.zeros(128, 64, dtype=scales))
+    with pytest.raises(ValueError, match=text + " must be (bf16|bytes|float32)"):
+        K.append_paged(x, w, m, ring, c, c, 4)
+    i64, i32 = torch.zeros(2, dtype=torch.int64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match=text):
+        K.tree_decode_paged(torch.zeros(3, 4, 512, dtype=torch.bfloat16), c, c, K.Cache(fmt, c.codes[None]), i32, i32, i64,
+                            100, 4)
+
+
+@pytest.mark.parametrize("fmt,codes,scales", [
+    (0, torch.bfloat16, None), (0, torch.uint16, None), (0, torch.int16, None), (1, torch.uint8, torch.float32),
+    (1, torch.float8_e4m3fn, torch.float32), (2, torch.int8, torch.float8_e4m3fn), (3, torch.uint8, torch.float32),
+])
+def test_the_binding_takes_every_spelling_of_a_format(fmt, codes, scales):
+    c = K.PagedCache(fmt, torch.zeros(128, 1024, dtype=codes), torch.zeros(2, 4, dtype=torch.int32), 64,
+                     None if scales is None else torch.zeros(128, 64, dtype=scales))
+    m = K.new_slot_map(2, 8, device="cpu")
+    with pytest.raises(ValueError, match="CUDA device"):        # the last check, behind those of the rows
+        K.append_paged(torch.zeros(8, 512, dtype=torch.bfloat16), torch.zeros(8, 512), m,
+                       torch.zeros(2, 136, 512, dtype=torch.bfloat16), c, c, 4)
