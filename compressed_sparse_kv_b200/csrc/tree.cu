@@ -207,6 +207,21 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
 }
+// The same for the end of a part of `tiles` tiles: 0.1 ms more for each, some 25 times what one takes.  (A role that is
+// stuck in one of them raises the flag after a second.)
+__device__ __noinline__ bool wait_part(uint64_t* bar, uint32_t parity, int tiles, volatile int* abort) {
+  const uint64_t t0 = globaltimer(), limit = kWaitLimitNs + 100000ull * uint64_t(tiles);
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
 // The products in flight after a wait gave up: bounded, abort or not.
 __device__ __noinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -607,11 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ queries
     bool ok = true;
+    int last = 0;  // tiles of the part before
     while (ok && next_part()) {
       load_part();
       const int row = p.idx ? (s.c0 + s.g) * p.heads + rank * ((p.heads + 1) / 2)
                             : s.c0 * p.heads + kGroup * s.g + rank * kQ;
-      if (segs > 0) ok = warp_wait(&ctl->o_done, (segs - 1) & 1, abort, lane);  // (the last part's scores have read theirs)
+      if (segs > 0) {  // (its scores have read its queries)
+        if (lane == 0) ok = wait_part(&ctl->o_done, (segs - 1) & 1, last, abort);
+        ok = __shfl_sync(kFull, ok, 0);
+      }
+      last = s.t1 - s.t0;
       if (ok && lane == 0) {
         // on the first CTA's barrier, or, to be converted first, on this one's
         if (C::kQuant) mbar_arrive_expect_tx(&ctl->q_full, kQBytes);

@@ -306,3 +306,23 @@ def test_zero_rows_beside_large_scales():
         c.comp_v[0][r] = 0.0
         c.comp.scales[at] = 0.0
     both(c)
+
+
+def test_a_part_of_half_a_million_tiles():
+    """A pair whose first part takes seconds goes on to its next one: the one-second limits are for single steps.  Every
+    entry lies in one page; with queries of zeros and rows of unit vectors all sums are whole numbers below 2^24."""
+    pairs, t, heads = torch.cuda.get_device_properties(0).multi_processor_count // 2, 1 << 26, 128
+    nodes = pairs + 1                                   # one group each: a long one a pair, and a short one behind them
+    codes = torch.zeros(64, 512, dtype=torch.uint8, device="cuda")
+    codes[torch.arange(512, device="cuda") % 64, torch.arange(512, device="cuda")] = 0x38       # 1.0
+    ones = lambda n: torch.ones(n, device="cuda")       # noqa: E731
+    comp = K.PagedCache(K.FP8_E4M3_ROW, codes, torch.zeros(2, t // 64, dtype=torch.int32, device="cuda"), 64, ones(64))
+    win = K.PagedCache(K.FP8_E4M3_ROW, codes[:0], torch.zeros(2, 1, dtype=torch.int32, device="cuda"), 64, ones(0))
+    draft = K.Cache(K.FP8_E4M3_ROW, torch.zeros(1, nodes, 512, dtype=torch.uint8, device="cuda"), ones(nodes)[None])
+    dev = lambda x, dt: torch.tensor(x, dtype=dt, device="cuda")    # noqa: E731
+    ws = K.new_workspace(K.tree_decode_paged_workspace_bytes(2, heads, pairs, nodes, t, 0, 1))
+    out = K.tree_decode_paged(torch.zeros(nodes, heads, 512, dtype=torch.bfloat16, device="cuda"), comp, win, draft,
+                              dev([0, pairs, nodes], torch.int32), dev([-1] * nodes, torch.int32),
+                              dev([t, 128], torch.int64), t, pairs, window=0, stride=1, rope_dim=0, out_fp32=True, ws=ws)
+    assert K.workspace_status(ws) == 0
+    assert torch.all(out == 1 / 64)
