@@ -90,7 +90,8 @@ constexpr float kNoMax = -3.4028235e38f;  // a maximum that nothing has reached 
 // Whole groups of 10 tiles against runs of 7: 37 against 48 us; 12 against 8 (selected, fp8): 77 against 62 us.
 constexpr int kSplitCost = 3;
 // Row scales below this are taken as it: the weight of a stored row carries its scale and the denominator divides it
-// out again, which needs a normal reciprocal.  Such a row's values are below 2^-91.
+// out again, which needs a normal reciprocal.  Such a row's fp8 values are below 2^-91 (and rotary ones in bf16 beside
+// them far outside of the range that the format's f16 staging keeps).
 constexpr float kMinScale = 0x1p-100f;
 
 constexpr int kValWarps = 4, kValRows = kRows / kValWarps;  // (a lane looks up one row)
@@ -369,7 +370,7 @@ __host__ __device__ constexpr int row_bytes(int fmt) {
 
 // Dequantises channels [ch0, ch0 + 256) of kR <= 32 rows (row i is lane i's `my`) to f16, in units of 16 bytes of codes:
 // 16 fp8 channels, 32 fp4 channels, or 8 bf16 rotary channels (stored as f16 of value / scale: the row's scale is in the
-// weights).  A batch is 8 units a lane: fetch() issues its loads, put() converts it.
+// weights; a scale of 0, which makes the fp8 channels zeros, is staged as 1: my_inv < 0).  A batch is 8 units a lane: fetch() issues its loads, put() converts it.
 template <int FMT, int kR>
 struct Dequant {
   static constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16, kFp4 = FMT == DSV4KV_FP4_E2M1_G16;
@@ -412,10 +413,14 @@ struct Dequant {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int x = 32 * (kN * batch + i) + lane, r = x / upr, u = x - r * upr;
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       float inv = 1.f;
       if constexpr (kRope) inv = __shfl_sync(kFull, my_inv, min(r, kR - 1));
       if (r >= kR) continue;
+      if (kRope && inv < 0.f) {
+        inv = -inv;
+        if (u < bd) w[0] = w[1] = w[2] = w[3] = 0u;
+      }
       if constexpr (kFp4) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -477,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sP = sV + kVBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(sP + kPBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr bool kRotary = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16;
   const int P = gridDim.x / 2, pair = blockIdx.x / 2;
   const int rank = int(cluster_rank());
   volatile int* abort = &ctl->abort;
@@ -1039,10 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         e.mysc = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
       if (C::kRowScale) {
         e.sr = src ? static_cast<const float*>(src->scales)[row] : 1.f;
-        if (e.sr == 0.f) {  // a row of zeros
-          e.sr = 1.f;
-          e.my = nullptr;
-        }
+        if (e.sr == 0.f && !kRotary) e.my = nullptr;  // a row of zeros
       }
     };
     while (ok && next_part()) {
@@ -1063,11 +1066,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const int r = kValRows * vw + lane;
           if (C::kRowScale) {
-            const float sr = cur.sr, at_least = fmaxf(sr, kMinScale);
+            const float sr = cur.sr == 0.f ? 1.f : cur.sr, at_least = fmaxf(sr, kMinScale);
             inv = 1.f / at_least;
             ctl->scale[sb][r] = sr;
             ctl->lscale[sb][r] = __log2f(at_least);
             ctl->iscale[sb][r] = inv;
+            if (kRotary && cur.sr == 0.f) inv = -inv;  // (zero but for its rotary channels)
           }
           ctl->key[sb][r] = cur.key;
           const uint32_t plain = __ballot_sync(kFull, cur.key.lo == 0 && cur.key.hi == kNever);
@@ -1160,8 +1164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         e.mysc = src ? static_cast<const uint8_t*>(src->scales) + size_t(row) * (kDim / 16) : nullptr;
       if (C::kRowScale) {
         const float sr = src ? static_cast<const float*>(src->scales)[row] : 1.f;
-        e.inv = 1.f / fmaxf(sr, kMinScale);
-        if (sr == 0.f) e.my = nullptr;  // a row of zeros
+        e.inv = sr == 0.f ? -1.f : 1.f / fmaxf(sr, kMinScale);  // (as the values')
+        if (sr == 0.f && !kRotary) e.my = nullptr;
       }
     };
     // the rows of a tile on their way to L2 (the keys' and the values' loads come after): two lanes a row

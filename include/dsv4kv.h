@@ -522,7 +522,8 @@ dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t bat
  * DSV4KV_DEV_BAD_TREE.  Rows no node of the call attends to are not read;
  * infinities and NaN in rows that one node does not see stay out of its output
  * (a row that it sees with a score of -infinity weighs nothing).
- * fp8 row scales are taken as at least 2^-100 (0: a row of zeros).
+ * fp8 row scales are taken as at least 2^-100; a scale of 0 means zeros (but for
+ * the rotary channels of DSV4KV_FP8_E4M3_ROW_ROPE_BF16, which have none).
  * Requirements: dim == 512; 1 <= heads <= 128; 1 <= max_nodes <= 256;
  * nodes * heads < 2^31; a pool of no pages only where no sequence up to t_max
  * can have a row of it; 1 <= batch <= 1024; the three caches of one format;

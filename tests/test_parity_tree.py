@@ -326,3 +326,20 @@ def test_a_part_of_half_a_million_tiles():
                               dev([t, 128], torch.int64), t, pairs, window=0, stride=1, rope_dim=0, out_fp32=True, ws=ws)
     assert K.workspace_status(ws) == 0
     assert torch.all(out == 1 / 64)
+
+
+@pytest.mark.parametrize("k", [0, 60])
+def test_zero_scales_beside_rotary_channels(k):
+    """A scale of 0 makes the fp8 channels zeros whatever their codes; the bf16 rotary channels have no scale."""
+    c = TreeCase(132, [900, 300], [4, 3], 16, K.FP8_E4M3_ROW_ROPE_BF16, stride=4, k=k)
+
+    def zero(cache, row, vals):
+        cache.scales.view(-1)[row] = 0.0
+        vals[:448] = 0.0
+    for b in range(2):
+        for r in range(0, len(c.comp_v[b]), 3):
+            zero(c.comp, int(c.comp.table[b, r // 64]) * 64 + r % 64, c.comp_v[b][r])
+        for r in (0, 7, 100):
+            zero(c.win, int(c.win.table[b, r // 64]) * 64 + r % 64, c.win_v[b][r])
+    zero(c.draft, 1, c.draft_v[0][1])
+    both(c)
