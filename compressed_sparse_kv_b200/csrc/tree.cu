@@ -368,6 +368,11 @@ __host__ __device__ constexpr int row_bytes(int fmt) {
                                       : kDim + 64;
 }
 
+// Two bf16 values times `by` as f16, finite ones saturating; infinities become NaN, as NaN stays NaN (x - x is 0 or NaN).
+__device__ __forceinline__ uint32_t staged(float lo, float hi, float by) {
+  return f32x2_to_f16x2_sat(fmaf(lo, by, lo - lo), fmaf(hi, by, hi - hi));
+}
+
 // Dequantises channels [ch0, ch0 + 256) of kR <= 32 rows (row i is lane i's `my`) to f16, in units of 16 bytes of codes:
 // 16 fp8 channels, 32 fp4 channels, or 8 bf16 rotary channels (stored as f16 of value / scale: the row's scale is in the
 // weights; a scale of 0, which makes the fp8 channels zeros, is staged as 1: my_inv < 0).  A batch is 8 units a lane: fetch() issues its loads, put() converts it.
@@ -434,7 +439,7 @@ struct Dequant {
       } else if (kRope && u >= bd) {
         uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = f32x2_to_f16x2_sat(bf16lo(w[e]) * inv, bf16hi(w[e]) * inv);
+        for (int e = 0; e < 4; ++e) h[e] = staged(bf16lo(w[e]), bf16hi(w[e]), inv);
         *reinterpret_cast<uint4*>(cell(r, kDim - 64 - ch0 + 8 * (u - bd))) = make_uint4(h[0], h[1], h[2], h[3]);
       } else {
         uint32_t h[8];
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 v = reinterpret_cast<uint4*>(sQ)[i];
             uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = f32x2_to_f16x2_sat(bf16lo(w[e]), bf16hi(w[e]));
+            for (int e = 0; e < 4; ++e) w[e] = staged(bf16lo(w[e]), bf16hi(w[e]), 1.f);
             reinterpret_cast<uint4*>(sQ)[i] = v;
           }
           fence_proxy_async_smem();

@@ -80,6 +80,8 @@ typedef enum {
  *                        values as f16 of value / scale, accurate while a row's rotary
  *                        values stay below 146 x the largest magnitude of its other
  *                        channels (the f16 range).
+ * With the quantised formats the decode calls multiply f16 operands: queries beyond
+ * +-65504 saturate (infinite ones too, except in dsv4kv_tree_decode_paged: NaN).
  */
 typedef enum {
   DSV4KV_BF16 = 0,
@@ -519,9 +521,11 @@ dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t bat
  * max_nodes (host) must be >= every m_b, t_max >= every t_b.  A cu entry that
  * descends, exceeds `nodes` or makes a tree larger than max_nodes is clamped and
  * sets DSV4KV_DEV_BAD_LENGTH; a parent outside [-1, i) is taken as -1 and sets
- * DSV4KV_DEV_BAD_TREE.  Rows no node of the call attends to are not read;
- * infinities and NaN in rows that one node does not see stay out of its output
- * (a row that it sees with a score of -infinity weighs nothing).
+ * DSV4KV_DEV_BAD_TREE.  Entries and window rows that no node attends to are not
+ * read (and no page is looked up for them).  Infinities and NaN in rows that a node
+ * does not see stay out of its output; a node that sees one, or whose query
+ * holds one, gives outputs that are not finite (only a row of infinities whose score
+ * is -infinity may weigh nothing instead).
  * fp8 row scales are taken as at least 2^-100; a scale of 0 means zeros (but for
  * the rotary channels of DSV4KV_FP8_E4M3_ROW_ROPE_BF16, which have none).
  * Requirements: dim == 512; 1 <= heads <= 128; 1 <= max_nodes <= 256;

@@ -343,3 +343,55 @@ def test_zero_scales_beside_rotary_channels(k):
             zero(c.win, int(c.win.table[b, r // 64]) * 64 + r % 64, c.win_v[b][r])
     zero(c.draft, 1, c.draft_v[0][1])
     both(c)
+
+
+BAD_ROWS = [(K.FP8_E4M3_ROW, "code", 0x7F), (K.FP8_E4M3_ROW, "scale", float("nan")), (K.FP8_E4M3_ROW, "scale", float("inf")),
+            (K.FP4_E2M1_G16, "scale", 0x7F), (K.FP8_E4M3_ROW_ROPE_BF16, "code", 0xFF),
+            (K.FP8_E4M3_ROW_ROPE_BF16, "scale", float("nan")),
+            (K.FP8_E4M3_ROW_ROPE_BF16, "scale", float("inf")), (K.FP8_E4M3_ROW_ROPE_BF16, "rotary", float("inf")),
+            (K.FP8_E4M3_ROW_ROPE_BF16, "rotary", float("-inf")), (K.FP8_E4M3_ROW_ROPE_BF16, "rotary", float("nan"))]
+
+
+@pytest.mark.parametrize("k", [0, 2])
+@pytest.mark.parametrize("heads", [64, 8])
+@pytest.mark.parametrize("fmt,where,bad", BAD_ROWS)
+def test_bad_quantised_rows_stay_with_the_nodes_that_see_them(fmt, where, bad, heads, k):
+    """As for bf16: a drafted row, a window row and an entry that only some nodes see, made non-finite one at a time."""
+    parents = [[-1, 0, 0, 2, 3]]                            # depths 0, 1, 1, 2, 3; node 1 is nobody's ancestor
+
+    case = lambda: TreeCase(140, [256 + 126], [5], heads, fmt, parents=parents, k=k)    # noqa: E731
+    want = case().run()
+    assert torch.isfinite(want).all()
+    # (window row 126 holds position 254, which depth 0 alone still sees; entry 1 is seen from depth 2 on)
+    for name, row, sees in (("draft", 2, [3, 4]), ("draft", 1, []), ("win", 126, [0]), ("comp", 1, [3, 4])):
+        c = case()
+        cache = getattr(c, name)
+        if name != "draft":
+            row = int(cache.table[0, row // 64]) * 64 + row % 64
+        codes = cache.codes.view(-1, cache.codes.shape[-1])
+        if where == "code":
+            codes[row, 300] = bad
+        elif where == "rotary":
+            codes.view(torch.bfloat16)[row, (448 + 2 * 11) // 2] = bad
+        else:
+            cache.scales.view(len(codes), -1)[row, -1] = bad
+        got = c.run()
+        for j in range(5):
+            if j in sees:
+                assert torch.isnan(got[j]).any(dim=-1).all(), (name, row, j)
+            else:
+                assert torch.equal(got[j], want[j]), (name, row, j)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("k", [0, 40])
+def test_a_query_that_is_not_finite(fmt, bad, k):
+    """Its own row is NaN, the others' are untouched."""
+    c = TreeCase(141, [300], [4], 16, fmt, stride=4, k=k)
+    want = c.run().clone()
+    c.q[1, 3, 11] = bad
+    got = c.run()
+    assert torch.isnan(got[1, 3]).all()
+    got[1, 3] = want[1, 3]
+    assert torch.equal(got, want)
