@@ -310,7 +310,8 @@ def _workspace(ws, nbytes: int, dev: int, where: str):
 
 
 def new_workspace(nbytes: int, device=None) -> torch.Tensor:
-    """Zero-filled workspace (the library leaves it zeroed after each call)."""
+    """Zero-filled workspace.  A call leaves it ready for the next one of its kind; decode calls leave partial sums in
+    it, so zero it again before an index call takes it over."""
     return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device or "cuda")
 
 

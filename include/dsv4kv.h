@@ -25,8 +25,14 @@
  *  - Workspaces: `*_workspace_bytes` gives the size; a workspace is 16-byte
  *    aligned (as every cudaMalloc'd block is; the decode calls return
  *    DSV4KV_ERR_INVALID_ARG otherwise), and it must be
- *    zero-filled once before its first use and is left in that state by every
- *    successful call, so it can be reused by the next call on the same stream.
+ *    zero-filled once before its first use.  Every successful call leaves it
+ *    ready for the next call of the same kind and sizes on the same stream, and,
+ *    index calls apart, for any other call that it is large enough for: the
+ *    decode calls (dsv4kv_tree_decode_paged among them) leave partial sums
+ *    behind the first 16 bytes, which only the index calls (dsv4kv_index_topk,
+ *    _score, _select, _topk_paged) need to be zero.  A buffer goes to an index call
+ *    after a decode call, or after an index call of another batch or length, only
+ *    when it has been zero-filled again.
  *    Calls that run concurrently need separate workspaces.  The first 4 bytes
  *    of a workspace are a sticky device status word: kernels OR the
  *    DSV4KV_DEV_* flags below into it and never trap or hang; the caller
@@ -522,7 +528,7 @@ dsv4kv_status dsv4kv_append_paged(const void* s_new, const float* w, int32_t bat
  * descends, exceeds `nodes` or makes a tree larger than max_nodes is clamped and
  * sets DSV4KV_DEV_BAD_LENGTH; a parent outside [-1, i) is taken as -1 and sets
  * DSV4KV_DEV_BAD_TREE.  Entries and window rows that no node attends to are not
- * read (and no page is looked up for them).  Infinities and NaN in rows that a node
+ * read (and their pages not flagged).  Infinities and NaN in rows that a node
  * does not see stay out of its output; a node that sees one, or whose query
  * holds one, gives outputs that are not finite (only a row of infinities whose score
  * is -infinity may weigh nothing instead).

@@ -395,3 +395,32 @@ def test_a_query_that_is_not_finite(fmt, bad, k):
     assert torch.isnan(got[1, 3]).all()
     got[1, 3] = want[1, 3]
     assert torch.equal(got, want)
+
+
+def test_one_workspace_for_the_decodes_and_the_serving_step():
+    """Every call but the index ones takes a workspace as another has left it; an index call takes it zero-filled."""
+    c = TreeCase(142, [20000], [2], 64, K.BF16, stride=4)
+    size = max(c.workspace().numel(), K.lib().dsv4kv_dense_decode_paged_workspace_bytes(1, 64, 512, c.t_max, 128, 4),
+               K.index_topk_workspace_bytes(3, 900, 64), K.paged_step_workspace_bytes(1))
+    ws, q = K.new_workspace(size), c.q[:1]
+    pages, one = K.PageTable(torch.full((1, 2), -1, dtype=torch.int32, device="cuda"), 64, 4), torch.tensor([0], device="cuda")
+    free, count = torch.arange(4, dtype=torch.int32, device="cuda"), torch.tensor([4], device="cuda")
+    qi = torch.randint(-8, 9, (3, 128), device="cuda").to(torch.bfloat16)
+    keys = K.Cache(0, torch.randint(-8, 9, (3, 900, 128), device="cuda").to(torch.bfloat16), None, 128)
+
+    def decode(w):
+        return K.dense_decode_paged(q, c.comp, c.win, c.t_seq, c.t_max, stride=4, ws=w)
+
+    def update(w):
+        K.block_table_update(one, one + 100, pages, free, count, 100, window=0, stride=1, ws=w)
+        return pages.table.clone()
+
+    calls = [c.run, decode, update]
+    want = [c.run(ws=c.workspace()).clone(), decode(K.new_workspace(size)), update(K.new_workspace(16))]
+    for i in (0, 1, 2, 0, 2, 1, 0):
+        assert torch.equal(calls[i](ws) if i else c.run(ws=ws), want[i]), i
+    assert K.workspace_status(ws) == 0 and ws[16:].any()
+    ws.zero_()
+    for a, b in zip(K.index_topk(qi, keys, 900, 64, ws=ws), K.index_topk(qi, keys, 900, 64)):
+        assert torch.equal(a, b)
+    assert torch.equal(c.run(ws=ws), want[0])
