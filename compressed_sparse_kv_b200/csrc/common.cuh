@@ -299,10 +299,14 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 // ----------------------------------------------------------------- CTA pairs (cta_group::2, clusters of two)
 // Address of `p` (shared memory of this CTA) in the pair's CTA of rank 0.
 __device__ __forceinline__ uint32_t lead_addr(const void* p) { return dsmem_addr(p, 0); }
-// Arrive on a barrier of either CTA of the pair (cluster address).  What the arriving thread hands over lies in its own
-// CTA's shared memory and is read there by the pair's products: the writers' proxy fence has completed those writes before
-// the arrival leaves, so the arrival is not given cluster scope (a cluster-wide release drains every outstanding
-// access of the SM: 1.3 us a tile under load).
+// Arrive on a barrier of either CTA of the pair (cluster address).  The release is at CTA scope, the instruction's
+// default, so the PTX memory model by itself does not order this CTA's writes before a wait in the other CTA.  Used here
+// on an assumption about the machine: what an arrival hands over (shared memory behind fence.proxy.async, TMEM behind
+// tcgen05.wait::st) lies in the arriving CTA's own SM, is complete there when those return, and is read there, by that
+// SM's part of the pair's products; the CTA that waits only issues them and reads none of it.  Nothing that the other
+// CTA's threads load may be handed over this way.  A release at cluster scope asks for no such assumption and costs, on
+// the softmax's arrivals alone, 213 -> 256 us (4 x 64 nodes at t = 2^20, bf16), with the loaders' 213 -> 258 and
+// 70 -> 75 (13 x 31 nodes, fp8).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
