@@ -508,3 +508,43 @@ def test_entries_outside_the_pool_are_not_given_back():
     out = K.block_table_update(dev([320, 128], torch.int64), dev([0, 0], torch.int64), p, fl, count, 320, window=0, stride=1,
                                ws=ws)
     assert K.workspace_status(ws) == K.DEV_BAD_PAGE and out.item() == 5 and fl[:5].tolist() == [3, 4, 6, 1, 2]
+
+
+@pytest.mark.parametrize("fmt", [f for f in FORMATS if f != K.BF16])
+@pytest.mark.parametrize("stride,taps", [(4, 8), (128, 128)])
+def test_appended_codes_are_the_nearest_ones(fmt, stride, taps):
+    """Scales are what the rows' largest magnitudes round to and codes the nearest to value / scale: no code further off
+    than the nearest, but for the error of the fp32 sums, rotation and quotient."""
+    a = Appender(300 + fmt + taps, 3, fmt, stride, taps, 128, 16, 1500)
+    for counts in ([900, 260, 300], [1, 2, 17], [0, 300, 5]):
+        a.step(counts)
+    e4m3 = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    e4m3 = np.unique(e4m3[np.isfinite(e4m3)])
+    e2m1 = np.array([-6, -4, -3, -2, -1.5, -1, -0.5, 0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+    def nearest(grid, x):
+        i = np.clip(np.searchsorted(grid, x), 1, len(grid) - 1)
+        return np.minimum(np.abs(grid[i - 1] - x), np.abs(grid[i] - x))
+
+    acc = (taps + 16) * 2.0 ** -24 * max(1.0, max(np.abs(h).max() for h in a.hist))
+    rows = 0
+    for cache, want in ((a.comp, a.want_c), (a.win, a.want_w)):
+        codes = cache.codes.cpu().numpy()
+        got = DEQUANT[fmt](codes, cache.scales.cpu().numpy())
+        for r, ref in want.items():
+            rows += 1
+            if fmt == K.FP4_E2M1_G16:
+                top = np.abs(ref).reshape(32, 16).max(1) / 6
+                s = cache.scales[r].cpu().view(torch.float8_e4m3fn).double().numpy()
+                assert np.all(np.abs(s - top) <= nearest(e4m3, top) + acc / 3 + 2.0 ** -23 * top)
+                s, grid, n = np.repeat(s, 16), e2m1, 512
+            else:
+                n, grid = 512 if fmt == K.FP8_E4M3_ROW else 448, e4m3
+                top, s = np.abs(ref[:n]).max() / 448, float(cache.scales[r])
+                assert abs(s - top) <= acc / 448 + 2.0 ** -23 * top
+            x = ref[:n] / np.where(s > 0, s, 1.0)
+            lim = s * nearest(grid, x) + 2 * acc + 2.0 ** -23 * np.abs(ref[:n])
+            off = np.abs(got[r, :n] - ref[:n])
+            assert np.all(off <= np.where(s > 0, lim, np.abs(ref[:n]))), (r, int(np.argmax(off - lim)))
+            assert np.all(np.abs(got[r, n:] - ref[n:]) <= acc + 2.0 ** -8 * np.abs(ref[n:]))
+    assert rows > 3 * 128
