@@ -12,7 +12,8 @@
 // and one launch does both: every CTA forms the prefix sums over the batch
 // (passes of warp scans in shared memory) and takes a share of the pages.
 // The count is read by every CTA and written by the last one to finish, so
-// that it may be updated in place.
+// that it may be updated in place; where some entries given back hold no page, that
+// CTA repeats the work with the others' ranks counted out.
 //
 // slot_map_kernel.  Every CTA forms the prefix sums of the new tokens, then a
 // thread finds the sequence of its first token by binary search and walks on;
@@ -98,6 +99,9 @@ __device__ __forceinline__ int64_t clamp_len(int64_t t, int64_t t_max, uint32_t*
   return t < 0 ? 0 : t_max;
 }
 
+// What a thread of block_table_kernel met: an entry without a page, a stack without one or without room, a bad page number.
+enum : uint32_t { kGap = 1, kNoRoom = 2, kBad = 4 };
+
 struct TableParams {
   const int64_t *t_old, *t_new;
   int batch;
@@ -123,7 +127,10 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TablePar
   extern __shared__ int32_t sm[];
   int32_t *back = sm, *take = back + p.batch + 1;          // prefix sums of the entries given back / taken
   int32_t *first = take + p.batch + 1, *good = first + p.batch + 1;  // a sequence's first such entry; see below
+  __shared__ uint32_t seen;
+  __shared__ bool again;
   pdl_trigger();
+  if (threadIdx.x == 0) seen = 0;
   pdl_wait();
   int64_t count = *p.free_count;
   if (count < 0 || count > p.free_cap) {
@@ -136,7 +143,6 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TablePar
         const int o = pages_of(p, clamp_len(p.t_old[b], p.t_max, p.status));
         const int n = pages_of(p, clamp_len(p.t_new[b], p.t_max, p.status));
         first[b] = min(o, n);
-        good[b] = 0;
         return o > n ? uint64_t(o - n) : uint64_t(n - o) << 32;
       },
       [&](int b, uint64_t v) {
@@ -148,79 +154,97 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TablePar
   __syncthreads();
   auto entry = [&](int b, int j) { return p.table[size_t(b) * p.table_stride + first[b] + j]; };
   auto is_page = [&](int32_t pg) { return pg >= 0 && pg < p.pool_pages; };
-  // Entries that hold no page (-1: the stack had none left when they were taken) are not given back.  Every CTA looks at
-  // all of them; where there are any, good[] becomes the prefix sums of the pages and the ranks below are counted out.
-  bool any = false;
-  for (int r = threadIdx.x; r < G; r += kTabThreads) {
-    const int b = find_seq(back, p.batch, r);
-    if (!is_page(entry(b, r - back[b]))) {
-      atomicAdd(&good[b], 1);
-      any = true;
-    }
-  }
-  any = __syncthreads_or(any);
-  int pages = G;
-  if (any) {
-    pages = int(block_prefix<kTabThreads>(
-        p.batch, [&](int b) -> uint64_t { return uint64_t(back[b + 1] - back[b] - good[b]); },
-        [&](int b, uint64_t v) { good[b] = int32_t(v); }));
-    if (threadIdx.x == 0) good[p.batch] = pages;
-    __syncthreads();
-  }
-  auto whole = [&](int b) { return good[b + 1] - good[b] == back[b + 1] - back[b]; };  // (where any)
-  const int step = gridDim.x * kTabThreads, begin = blockIdx.x * kTabThreads + int(threadIdx.x);
-  // page number r of those given back
-  auto given = [&](int r) -> int32_t {
-    const int b = find_seq(any ? good : back, p.batch, r);
-    int j = r - (any ? good[b] : back[b]);
-    if (any && !whole(b)) {
-      int k = j;
-      for (j = 0; !is_page(entry(b, j)) || k-- > 0;) ++j;  // (ends: the sequence gives back more than k pages)
-    }
-    return entry(b, j);
-  };
-  for (int x = begin; x < G; x += step) {
-    const int b = find_seq(back, p.batch, x), j = x - back[b];
-    const int32_t pg = entry(b, j);
-    if (!is_page(pg)) {
-      if (pg != -1) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
-      continue;
-    }
-    int r = x;
-    if (any) {
-      r = good[b] + j;
-      if (!whole(b))
-        for (int i = 0; i < j; ++i) r -= !is_page(entry(b, i));
-    }
-    if (count + r < p.free_cap) p.free_pages[count + r] = pg;
-    else set_status(p.status, DSV4KV_DEV_NO_PAGES);
-  }
-  const int64_t top = min(count + pages, p.free_cap);  // the grown stack
-  for (int a = begin; a < A; a += step) {
-    const int b = find_seq(take, p.batch, a);
-    const int64_t at = top - 1 - a;
-    int32_t pg = -1;
-    if (at < 0) {
-      set_status(p.status, DSV4KV_DEV_NO_PAGES);
-    } else {
-      pg = at >= count ? given(int(at - count)) : p.free_pages[at];
-      if (!is_page(pg)) {
-        set_status(p.status, DSV4KV_DEV_BAD_PAGE);
-        pg = -1;
+  // The pushes and pops of threads begin, begin + step, ..; `pages` of the G entries given back hold one: all of them, or
+  // (gaps) those that the prefix sums good[] count.  Returns what it met.
+  auto move_pages = [&](int begin, int step, bool gaps, int pages) -> uint32_t {
+    uint32_t met = 0;
+    auto whole = [&](int b) { return !gaps || good[b + 1] - good[b] == back[b + 1] - back[b]; };
+    auto given = [&](int r) -> int32_t {  // page r of those given back
+      const int b = find_seq(gaps ? good : back, p.batch, r);
+      int j = r - (gaps ? good[b] : back[b]);
+      if (!whole(b)) {
+        int k = j;
+        for (j = 0; !is_page(entry(b, j)) || k-- > 0;) ++j;  // (ends: the sequence gives back more than k pages)
       }
+      return entry(b, j);
+    };
+    for (int x = begin; x < G; x += step) {
+      const int b = find_seq(back, p.batch, x), j = x - back[b];
+      const int32_t pg = entry(b, j);
+      if (!is_page(pg)) {
+        met |= pg == -1 ? kGap : kGap | kBad;
+        continue;
+      }
+      int r = x;
+      if (gaps) {
+        r = good[b] + j;
+        if (!whole(b))
+          for (int i = 0; i < j; ++i) r -= !is_page(entry(b, i));
+      }
+      if (count + r < p.free_cap) p.free_pages[count + r] = pg;
+      else met |= kNoRoom;
     }
-    p.table[size_t(b) * p.table_stride + first[b] + (a - take[b])] = pg;
-  }
-  // the last CTA to get here (every CTA has read the count) writes it
+    const int64_t top = min(count + pages, p.free_cap);  // the grown stack
+    for (int a = begin; a < A; a += step) {
+      const int b = find_seq(take, p.batch, a);
+      const int64_t at = top - 1 - a;
+      int32_t pg = -1;
+      if (at < 0) {
+        met |= kNoRoom;
+      } else {
+        pg = at >= count ? given(int(at - count)) : p.free_pages[at];
+        if (!is_page(pg)) {
+          met |= kBad;
+          pg = -1;
+        }
+      }
+      p.table[size_t(b) * p.table_stride + first[b] + (a - take[b])] = pg;
+    }
+    return met;
+  };
+  uint32_t met = move_pages(blockIdx.x * kTabThreads + int(threadIdx.x), gridDim.x * kTabThreads, false, G);
+  if (met) atomicOr(&seen, met);
   __syncthreads();
+  auto finish = [&](uint32_t flags, int pages) {
+    if (flags & kNoRoom) set_status(p.status, DSV4KV_DEV_NO_PAGES);
+    if (flags & kBad) set_status(p.status, DSV4KV_DEV_BAD_PAGE);
+    *p.free_count_out = max(int64_t(0), min(count + pages, p.free_cap) - A);
+  };
+  // The last CTA to get here (every CTA has read the count) writes it, and the flags of all (a byte of the counter each).
   if (threadIdx.x == 0) {
     __threadfence();
     uint32_t* done = p.status + 1;
-    if (atomicAdd(done, 1u) == gridDim.x - 1) {
+    const uint32_t own = 1u + (seen & kGap ? 0x100u : 0u) + (seen & kNoRoom ? 0x10000u : 0u) + (seen & kBad ? 0x1000000u : 0u);
+    const uint32_t all = atomicAdd(done, own) + own;
+    again = false;
+    if ((all & 0xffu) == gridDim.x) {
       *done = 0;
-      *p.free_count_out = max(int64_t(0), top - A);
+      again = (all & 0xff00u) != 0;
+      if (!again) finish((all & 0xff0000u ? kNoRoom : 0u) | (all & 0xff000000u ? kBad : 0u), G);
     }
   }
+  __syncthreads();
+  if (!again) return;
+  // Some entries held no page (the stack had none left when they were taken) and belong not on it: the CTA does all
+  // pushes and pops again with the others counted out.  What was written so far lies above the old stack and in the
+  // entries taken, none of it read.
+  __threadfence();
+  for (int b = threadIdx.x; b < p.batch; b += kTabThreads) good[b] = 0;
+  if (threadIdx.x == 0) seen = 0;
+  __syncthreads();
+  for (int x = threadIdx.x; x < G; x += kTabThreads) {
+    const int b = find_seq(back, p.batch, x);
+    if (is_page(entry(b, x - back[b]))) atomicAdd(&good[b], 1);
+  }
+  __syncthreads();
+  const int pages = int(block_prefix<kTabThreads>(
+      p.batch, [&](int b) -> uint64_t { return uint64_t(good[b]); }, [&](int b, uint64_t v) { good[b] = int32_t(v); }));
+  if (threadIdx.x == 0) good[p.batch] = pages;
+  __syncthreads();
+  met = move_pages(threadIdx.x, kTabThreads, true, pages);
+  if (met) atomicOr(&seen, met);
+  __syncthreads();
+  if (threadIdx.x == 0) finish(seen, pages);
 }
 
 // Quotients by a divisor of the whole call: floor(n / d) is the high word of n * (floor((2^64 - 1) / d) + 1) for all 32-bit
