@@ -19,14 +19,17 @@
 // thread finds the sequence of its first token by binary search and walks on;
 // 4 tokens a thread, 16-byte stores.
 //
-// (48 prompts of up to 65,536 tokens, about 1.7 M in all: tables and map 19.5 us for 35 MB, bound by start-up and searches; a decode step of
-// 32 sequences: 7.2 us, two launches' latency.  Plain integer divisions: 21.3 and 8.0.)
+// (Times here are of a replayed graph of ten calls; one after another, calls of
+// a few us are bound by the host, the prompts take 3 to 4 us more.)  48 prompts of
+// up to 65,536 tokens, about 1.7 M in all: tables and map 18.5 us for 35 MB, bound by
+// start-up and searches; a decode step of 32 sequences: 7.2 us, two launches'
+// latency.  Plain integer divisions in the map: 1.8 and 0.8 us more.
 //
 // append_paged_kernel (entries of up to 32 taps).  A CTA of 8 warps takes `per`
 // consecutive tokens.  It lists the tokens whose row stays in a ring and those
 // that emit an entry; a warp copies / rotates one row or sums one entry
 // (16 channels a lane, the weights in shared memory, packed fp32 multiply-adds).
-// Whole prompts are bound by instructions and the rows' HBM reads: 75,000
+// Whole prompts are bound by the latency of the rows' reads at 16 warps an SM: 75,000
 // tokens of c4a, 96 MB, in 31 us (3.1 TB/s, its second launch included); a step
 // of 32 sequences x 8 tokens, 5.3 us, is latency.  Taps loaded one address at
 // a time and scalar multiply-adds: 38 us; 3 CTAs an SM at 80 registers: 42.

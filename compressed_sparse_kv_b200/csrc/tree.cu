@@ -38,11 +38,13 @@
 //
 // What bounds it: a buffer's round (product done, copy issued, rows here, product
 // issued), since keys and values have one buffer each in two halves.  Measured
-// per tile of 128 rows and pair of CTAs: 2.2 us for whole bf16 tiles (256 x 64
-// query rows x 8,320 rows x 4 sequences: 216 us, 856 TFLOP/s; the products alone
-// would take 1.0 us), 3.2 us for selected bf16 rows, 4.2 us for fp8 rows.
-// 18 us of latency for one short sequence: 4 us until the schedule and the tree
-// are known, two tiles of 4 us each (not overlapped), 3 us to finish.
+// per tile of 128 rows and pair of CTAs: 2.2 us for whole bf16 tiles (the products
+// alone would take 1.0 us), 3.2 us for selected bf16 rows, 4.2 us for fp8 rows.
+// 256 x 64 query rows x 8,320 bf16 rows x 4 sequences: 245 us called one after
+// another (750 TFLOP/s), 215 us in a replayed graph of ten, where a call's set-up
+// runs beside the one before.  18 us of latency for one short sequence: 4 us until
+// the schedule and the tree are known, two tiles of 4 us each (not overlapped), 3 us
+// to finish.
 //
 // Work split.  When the groups fill the pairs evenly a pair takes whole groups
 // (c, c + P, ...); otherwise the tiles of all groups are laid end to end and cut
@@ -87,7 +89,8 @@ constexpr uint32_t kColS = 256;  // S: 2 buffers of 64 columns
 constexpr float kRaise = 8.0f;   // log2 units a score may pass the running maximum by
 constexpr float kNoMax = -3.4028235e38f;  // a maximum that nothing has reached yet (finite: x - m of a hidden row is -inf)
 // Tiles that cut groups may cost (partial sums, a second part per pair, the merge) before whole groups take longer.
-// Whole groups of 10 tiles against runs of 7: 37 against 48 us; 12 against 8 (selected, fp8): 77 against 62 us.
+// Whole groups of 10 bf16 tiles against runs of 7: 37 against 48 us; 12 fp8 tiles against 8: 77 against 62 us.  Over 208
+// combinations of 8 to 230 groups of 2 to 40 tiles, in bf16 and fp8, 3 is 1.1 % off the faster choice on average.
 constexpr int kSplitCost = 3;
 // Row scales below this are taken as it: the weight of a stored row carries its scale and the denominator divides it
 // out again, which needs a normal reciprocal.  Such a row's fp8 values are below 2^-91 (and rotary ones in bf16 beside

@@ -88,6 +88,9 @@ typedef enum {
  *                        channels (the f16 range).
  * With the quantised formats the decode calls multiply f16 operands: queries beyond
  * +-65504 saturate (infinite ones too, except in dsv4kv_tree_decode_paged: NaN).
+ * With a scale per row a row's weight carries its scale, in f16 and relative to the
+ * largest such product: rows whose weight x scale is below 2^-14 of that (beside a row
+ * of zeros, whose scale dsv4kv_quantize makes 1, say) lose precision, below 2^-25 their place.
  */
 typedef enum {
   DSV4KV_BF16 = 0,
