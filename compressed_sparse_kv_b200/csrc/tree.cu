@@ -378,7 +378,8 @@ __device__ __forceinline__ uint32_t staged(float lo, float hi, float by) {
 
 // Dequantises channels [ch0, ch0 + 256) of kR <= 32 rows (row i is lane i's `my`) to f16, in units of 16 bytes of codes:
 // 16 fp8 channels, 32 fp4 channels, or 8 bf16 rotary channels (stored as f16 of value / scale: the row's scale is in the
-// weights; a scale of 0, which makes the fp8 channels zeros, is staged as 1: my_inv < 0).  A batch is 8 units a lane: fetch() issues its loads, put() converts it.
+// weights; a scale of 0, which makes the fp8 channels zeros, is staged as 1: my_inv < 0).  A batch is 8 units a lane:
+// fetch() issues its loads, put() converts it.
 template <int FMT, int kR>
 struct Dequant {
   static constexpr bool kRope = FMT == DSV4KV_FP8_E4M3_ROW_ROPE_BF16, kFp4 = FMT == DSV4KV_FP4_E2M1_G16;
